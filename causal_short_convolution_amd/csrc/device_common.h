@@ -1,12 +1,15 @@
 // Device helpers shared by the HIP kernels of the fused ShortConv K/V step (forward, speculative
 // verification, MXFP8 encoding and backward): element types, 16-byte row access with streaming
-// hints, cross-lane moves and reductions, and the tile -> sequence search of the prefill grids.
+// hints, cross-lane moves and reductions, the tile -> sequence search of the prefill grids, the row
+// math and the cache row formats.
 // Internal to the library; not part of the C ABI.
 #ifndef SHORTCONV_DEVICE_COMMON_H
 #define SHORTCONV_DEVICE_COMMON_H
 
 #include <hip/hip_runtime.h>
 #include <stdint.h>
+
+#include "shortconv_internal.h"
 
 namespace sc {
 
@@ -209,6 +212,203 @@ __device__ inline int tile_seq_bounds(const int32_t* cu, int n, int64_t T, int64
     end = uniform((int64_t)clamp_tok(cu[s + 1], T));
     return s;
 }
+
+// ------------------------------------------------------------------------------------------------
+// The row math and the cache row formats (prefill, decode, verification of chains and trees).
+// ------------------------------------------------------------------------------------------------
+// Per-lane constants of one (tensor, head, 16-byte column) position.
+template <class E, int W>
+struct LaneParams {
+    float tap[W][E::VEC];
+    float gam[E::VEC];
+};
+
+template <class E, int W>
+__device__ inline void load_params(const float* taps, const float* gamma, int heads, int D, int h,
+                                   int d0, LaneParams<E, W>& p) {
+#pragma unroll
+    for (int k = 0; k < W; ++k) {
+        const float* t = taps + ((int64_t)k * heads + h) * D + d0;
+#pragma unroll
+        for (int v = 0; v < E::VEC; v += 4) {
+            const float4 q = *reinterpret_cast<const float4*>(t + v);
+            p.tap[k][v] = q.x;
+            p.tap[k][v + 1] = q.y;
+            p.tap[k][v + 2] = q.z;
+            p.tap[k][v + 3] = q.w;
+        }
+    }
+#pragma unroll
+    for (int v = 0; v < E::VEC; v += 4) {
+        const float4 q = *reinterpret_cast<const float4*>(gamma + d0 + v);
+        p.gam[v] = q.x;
+        p.gam[v + 1] = q.y;
+        p.gam[v + 2] = q.z;
+        p.gam[v + 3] = q.w;
+    }
+}
+
+// The row math of one output row slice: window row k (k = W-1 is the current token) is
+// win[(off + k) % W], off being a compile-time constant after unrolling; o gets the normalized
+// values in fp32, before the one rounding to the cache format.
+template <class E, int W, int LPH>
+__device__ inline void fused_row(const float (&win)[W][E::VEC], int off,
+                                 const LaneParams<E, W>& p, float eps, float inv_d,
+                                 float (&o)[E::VEC]) {
+    constexpr int VEC = E::VEC;
+    float c[VEC];
+#pragma unroll
+    for (int v = 0; v < VEC; ++v) c[v] = p.tap[0][v] * win[off % W][v];
+#pragma unroll
+    for (int k = 1; k < W; ++k)
+#pragma unroll
+        for (int v = 0; v < VEC; ++v)
+            c[v] = __builtin_fmaf(p.tap[k][v], win[(off + k) % W][v], c[v]);
+    float ss = 0.0f;
+#pragma unroll
+    for (int v = 0; v < VEC; ++v) ss = __builtin_fmaf(c[v], c[v], ss);
+    ss = head_sum<LPH>(ss);
+    // v_rsq_f32: within ~1 ulp of 1/sqrt, one instruction instead of a correctly rounded square
+    // root and divide; it scales exactly under power-of-4 scaling of its input.
+    const float inv = __builtin_amdgcn_rsqf(__builtin_fmaf(ss, inv_d, eps));
+#pragma unroll
+    for (int v = 0; v < VEC; ++v) o[v] = (c[v] * inv) * p.gam[v];
+}
+
+// ------------------------------------------------------------------------------------------------
+// Cache formats. A Sink takes one finished row slice (VEC fp32 values of one head) and writes it
+// to cache row `slot`, unless the slot is outside [0, num_slots) or the lane is idle.
+// ------------------------------------------------------------------------------------------------
+// Plain rows in the I/O element type (one round-to-nearest-even conversion).
+template <class E>
+struct PlainSink {
+    char* cache;
+    int64_t row_bytes;
+    uint32_t lane_off;
+    int64_t num_slots;
+    __device__ PlainSink(const StepArgs& a, int tensor, int h, int d0, int D)
+        : cache(static_cast<char*>(pick(a.cache, tensor))),
+          row_bytes((int64_t)a.heads * D * E::BYTES),
+          lane_off((uint32_t)(((int64_t)h * D + d0) * E::BYTES)),
+          num_slots(a.num_slots) {}
+    // A row slice in its stored form, and its store (skipped for an idle lane or a slot outside
+    // the pool).
+    using Enc = uint4;
+    __device__ Enc encode(const float (&o)[E::VEC]) const { return E::narrow(o); }
+    // The slot is wave-uniform in every caller; its byte offset is kept scalar (read through
+    // readfirstlane), so the address is one add to the lane's base instead of a 64-bit
+    // multiply-add on the vector unit at quarter rate.
+    __device__ void write(int64_t slot, bool active, const Enc& out) const {
+        if (active && slot >= 0 && slot < num_slots)
+            strow(cache + uniform(slot * row_bytes), lane_off, out);
+    }
+    __device__ void put(int64_t slot, bool active, const float (&o)[E::VEC]) const {
+        write(slot, active, encode(o));
+    }
+};
+
+// OCP FP8 E4M3 codes of v[b] * 2^-e for four finite values (byte b): nearest value, ties to even,
+// saturating at +-448. gfx950's scaled conversion (v_cvt_scalef32_pk_fp8_f32) divides by its
+// scale operand, here 2^e, exactly and rounds to nearest even into the OCP format, but does not
+// saturate; clamping v to +-448 * 2^e first is the same as clamping v * 2^-e to +-448, scaling by
+// a power of two being exact.
+typedef short sc_i16x2 __attribute__((ext_vector_type(2)));
+__device__ inline uint32_t e4m3x4_scaled(float v0, float v1, float v2, float v3, float scale,
+                                         float lim) {
+    v0 = __builtin_amdgcn_fmed3f(v0, -lim, lim);
+    v1 = __builtin_amdgcn_fmed3f(v1, -lim, lim);
+    v2 = __builtin_amdgcn_fmed3f(v2, -lim, lim);
+    v3 = __builtin_amdgcn_fmed3f(v3, -lim, lim);
+    // the two conversions write the low and the high half; the word they start from (any
+    // register at hand) is overwritten entirely
+    sc_i16x2 w = __builtin_bit_cast(sc_i16x2, __float_as_uint(v0));
+    w = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(w, v0, v1, scale, false);
+    w = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(w, v2, v3, scale, true);
+    return __builtin_bit_cast(uint32_t, w);
+}
+
+// The MXFP8 encoding of one lane's VEC values: the maximum over the 32/VEC lanes of a 32-element
+// block (DPP), the E8M0 exponent e = floor(log2(max)) - 8 clamped to [-127, 127] (-127 for an
+// all-zero block), and the saturated E4M3 codes of v * 2^-e. Across lanes the maximum of the
+// magnitudes is taken on their bit patterns, which order non-negative finite floats as unsigned
+// integers do; the pattern's exponent field E gives floor(log2(max)) = E - 127 for a normal
+// maximum, so e = E - 135, which is at most 119, and every zero or subnormal maximum (E = 0)
+// falls to the clamp at -127.
+template <class E>
+struct MxEnc {
+    uint32_t packed[E::VEC / 4];
+    int e;
+};
+template <class E>
+__device__ inline MxEnc<E> mx_encode(const float (&o)[E::VEC]) {
+    constexpr int VEC = E::VEC;
+    constexpr int LPB = 32 / VEC;
+    float amax = 0.0f;
+#pragma unroll
+    for (int v = 0; v < VEC; ++v) amax = __builtin_fmaxf(amax, __builtin_fabsf(o[v]));
+    uint32_t bits = __float_as_uint(amax);
+    bits = max(bits, dpp_u32<kQuadXor1>(bits));
+    bits = max(bits, dpp_u32<kQuadXor2>(bits));
+    if (LPB == 8) bits = max(bits, dpp_u32<kRowHalfMirror>(bits));
+    MxEnc<E> r;
+    const int e = max((int)(bits >> 23) - 135, -127);
+    r.e = e;
+    const float scale = __builtin_ldexpf(1.0f, e);
+    const float lim = __builtin_ldexpf(448.0f, e);  // +inf at e = 127: nothing saturates there
+#pragma unroll
+    for (int q = 0; q < VEC / 4; ++q)
+        r.packed[q] = e4m3x4_scaled(o[4 * q], o[4 * q + 1], o[4 * q + 2], o[4 * q + 3], scale, lim);
+    return r;
+}
+
+// MXFP8 rows: 32-element blocks along head_dim share one E8M0 scale 2^e with
+// e = floor(log2(max |v|)) - 8 (clamped to [-127, 127]; -127 for an all-zero block), and each
+// element is stored as the E4M3 code of v * 2^-e. Codes [num_slots][H][D] bytes, scales
+// [num_slots][H][D/32] bytes (e + 127). The 32/VEC lanes of a block exchange their maxima by DPP.
+template <class E>
+struct MxSink {
+    static constexpr int VEC = E::VEC;
+    static constexpr int LPB = 32 / VEC;  // lanes per block: 4 (bf16) or 8 (fp32)
+    char* codes;
+    char* scales;
+    int64_t row_elems;
+    uint32_t code_off;
+    uint32_t scale_off;
+    bool scale_lane;
+    int64_t num_slots;
+    __device__ MxSink(const StepArgs& a, int tensor, int h, int d0, int D)
+        : codes(static_cast<char*>(pick(a.cache, tensor))),
+          scales(static_cast<char*>(pick(a.scales, tensor))),
+          row_elems((int64_t)a.heads * D),
+          code_off((uint32_t)((int64_t)h * D + d0)),
+          scale_off((uint32_t)(((int64_t)h * D + d0) / 32)),
+          scale_lane(d0 % 32 == 0),
+          num_slots(a.num_slots) {}
+    using Enc = MxEnc<E>;  // the VEC codes, 4 per word, and the block's scale exponent
+    __device__ Enc encode(const float (&o)[VEC]) const { return mx_encode<E>(o); }
+    __device__ void write(int64_t slot, bool active, const Enc& enc) const {
+        if (!(active && slot >= 0 && slot < num_slots)) return;
+        char* row = codes + uniform(slot * row_elems) + code_off;  // (offset kept scalar)
+        if (VEC == 8) {
+            typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+            const u32x2 w = {enc.packed[0], enc.packed[VEC / 4 - 1]};
+            __builtin_nontemporal_store(w, reinterpret_cast<u32x2*>(row));
+        } else {
+            __builtin_nontemporal_store(enc.packed[0], reinterpret_cast<uint32_t*>(row));
+        }
+        if (scale_lane)
+            *reinterpret_cast<uint8_t*>(scales + uniform(slot * (row_elems / 32)) + scale_off) =
+                (uint8_t)(enc.e + 127);
+    }
+    __device__ void put(int64_t slot, bool active, const float (&o)[VEC]) const {
+        write(slot, active, encode(o));
+    }
+};
+
+template <class E, bool MX>
+struct SinkFor { using type = PlainSink<E>; };
+template <class E>
+struct SinkFor<E, true> { using type = MxSink<E>; };
 
 }  // namespace sc
 
