@@ -1,10 +1,12 @@
-"""Build libshortconv.so (the C-ABI library with the gfx950 kernels) in-tree with hipcc.
+"""Build libshortconv.so and libshortconv_cache.so (the C-ABI libraries with the gfx950 kernels:
+the fused step, and the operators on the cache it writes) in-tree with hipcc.
 
     python -m causal_short_convolution_amd.build [--save-temps DIR]
 
 Flags: gfx950 only; -ffp-contract=off so the kernels' fused multiply-adds are exactly the
 explicit ones; packed-fp32 instruction selection disabled; hidden visibility so the library
-exports only the extern "C" entry points declared in include/shortconv.h.
+exports only the extern "C" entry points declared in its header (include/shortconv.h,
+include/shortconv_cache.h).
 """
 import argparse
 import os
@@ -15,6 +17,11 @@ ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libshortconv.so")
 SOURCES = [os.path.join(CSRC, f) for f in ("kernels.hip", "backward.hip", "abi.hip")]
+# the operators on the paged cache, a library of its own (include/shortconv_cache.h)
+CACHE_LIB = os.path.join(HERE, "libshortconv_cache.so")
+CACHE_SOURCES = [os.path.join(CSRC, f) for f in ("tree_verify.hip", "cache_attention.hip",
+                                                 "cache_blocks.hip", "cache_evict.hip",
+                                                 "cache_abi.hip")]
 # measurement companion used by bench.py (same-bytes copy ceiling); not part of the C ABI
 PROBE_LIB = os.path.join(HERE, "libscprobe.so")
 PROBE_SOURCES = [os.path.join(CSRC, "copy_probe.hip")]
@@ -33,7 +40,7 @@ FLAGS = [
 
 def _hipcc(out, sources, verbose, save_temps=None):
     tmp = out + ".tmp"
-    cmd = [HIPCC, *FLAGS, "-I", os.path.join(ROOT, "include"), "-I", CSRC, "-o", tmp, *sources]
+    cmd = [HIPCC, *FLAGS, f"-parallel-jobs={min(8, len(sources))}", "-I", os.path.join(ROOT, "include"), "-I", CSRC, "-o", tmp, *sources]
     cwd = None
     if save_temps:
         os.makedirs(save_temps, exist_ok=True)
@@ -47,6 +54,7 @@ def _hipcc(out, sources, verbose, save_temps=None):
 
 def build(verbose: bool = False, save_temps: str = None) -> str:
     _hipcc(LIB, SOURCES, verbose, save_temps)
+    _hipcc(CACHE_LIB, CACHE_SOURCES, verbose, save_temps)
     _hipcc(PROBE_LIB, PROBE_SOURCES, verbose)
     return LIB
 

@@ -1,0 +1,162 @@
+// Device helpers of the cache operators: the sequence of a token, page lookup, and the selection
+// of the largest keys of a list.
+#ifndef SHORTCONV_CACHE_DEVICE_H
+#define SHORTCONV_CACHE_DEVICE_H
+
+#include "cache_internal.h"
+#include "device_common.h"
+
+namespace sc {
+
+// The largest s in [0, n) with clamp(cu[s]) <= t (0 if none), by whole waves: each round 64 lanes
+// test 64 evenly spaced candidates, as in find_tile_seq.
+__device__ inline int seq_of_token(const Batch& b, int64_t t) {
+    const int wl = threadIdx.x & 63;
+    int base = 0, count = b.num_seqs;
+    while (count > 1) {
+        const int step = (count + 63) / 64;
+        const bool ok = wl * step < count && clamp_tok(b.cu[base + wl * step], b.tokens) <= t;
+        const uint64_t mask = __ballot(ok);
+        const int last = mask ? 63 - __builtin_clzll(mask) : 0;
+        base += last * step;
+        count = step < count - last * step ? step : count - last * step;
+    }
+    return uniform(base);
+}
+
+// One sequence of a batch: its new tokens [start, start + len), its cached keys, and the number
+// of keys in all, which the page table bounds.
+struct SeqInfo {
+    int64_t start;
+    int32_t len;
+    int32_t ctx;
+    int32_t keys;
+};
+__device__ inline SeqInfo seq_info(const Batch& b, const Paging& pg, int s) {
+    SeqInfo r;
+    const int32_t c0 = clamp_tok(b.cu[s], b.tokens);
+    const int32_t c1 = clamp_tok(b.cu[s + 1], b.tokens);
+    const int32_t cap = pg.max_blocks << pg.shift;
+    const int32_t ctx = b.ctx[s];
+    r.start = c0;
+    r.len = c1 > c0 ? c1 - c0 : 0;
+    r.ctx = ctx < 0 ? 0 : (ctx > cap ? cap : ctx);
+    r.keys = r.len < cap - r.ctx ? r.ctx + r.len : cap;
+    return r;
+}
+
+// The cache row of position p (0 <= p < max_blocks << shift), or -1 where the page is outside the
+// pool.
+__device__ inline int32_t slot_of(const Paging& pg, int s, int32_t p) {
+    const int32_t page = pg.table[(int64_t)s * pg.max_blocks + (p >> pg.shift)];
+    const bool ok = page >= 0 && page < pg.num_pages;
+    return ok ? (page << pg.shift) + (p & ((1 << pg.shift) - 1)) : -1;
+}
+
+// Maximum over the LPH lanes of a head of values whose bit patterns order as unsigned integers
+// (magnitudes of floats).
+template <int LPH>
+__device__ inline uint32_t head_max(uint32_t v) {
+    v = max(v, dpp_u32<kQuadXor1>(v));
+    v = max(v, dpp_u32<kQuadXor2>(v));
+    v = max(v, dpp_u32<kRowHalfMirror>(v));
+    if (LPH >= 16) v = max(v, dpp_u32<kRowMirror>(v));
+    if (LPH >= 32) {
+        const auto p = __builtin_amdgcn_permlane16_swap(v, v, false, false);
+        v = max((uint32_t)p[0], (uint32_t)p[1]);
+    }
+    if (LPH >= 64) {
+        const auto p = __builtin_amdgcn_permlane32_swap(v, v, false, false);
+        v = max((uint32_t)p[0], (uint32_t)p[1]);
+    }
+    return v;
+}
+
+// Floats as unsigned integers in the same order (no NaN; -0 counts as +0).
+__device__ inline uint32_t order_key(float f) {
+    const uint32_t u = __float_as_uint(f + 0.0f);
+    return (u >> 31) ? ~u : (u | 0x80000000u);
+}
+
+// The exponent E of a group of values whose largest magnitude has the bit pattern `top`:
+// floor(log2) - 6, at least -127, so that the magnitude times 2^-E lies in [64, 128).
+__device__ inline int code_exponent(uint32_t top) { return max((int)(top >> 23) - 133, -127); }
+
+// One value as a whole number in +-127 under the exponent E.
+__device__ inline float code_of(float x, int e) {
+    return __builtin_amdgcn_fmed3f(__builtin_rintf(__builtin_ldexpf(x, -e)), -127.0f, 127.0f);
+}
+
+// The k-th largest of n keys, by one workgroup, 8 bits at a time: `threshold` is its value and
+// `ties` how many keys equal to it belong to the k largest. 1 <= k <= n. `hist` is LDS of
+// 256 + 2 words; key(i) gives key i. Every thread of the workgroup takes part, and all return the
+// same. The counts are whole numbers, so the order of the atomics does not matter.
+template <class Key>
+__device__ inline void kth_largest(Key key, int n, int k, uint32_t* hist, uint32_t& threshold,
+                                   int& ties) {
+    uint32_t prefix = 0;
+    int rest = k;
+    for (int shift = 24; shift >= 0; shift -= 8) {
+        for (int i = threadIdx.x; i < 256; i += blockDim.x) hist[i] = 0;
+        __syncthreads();
+        for (int i = threadIdx.x; i < n; i += blockDim.x) {
+            const uint32_t x = key(i);
+            if (shift == 24 || (x >> (shift + 8)) == (prefix >> (shift + 8)))
+                atomicAdd(&hist[(x >> shift) & 255u], 1u);
+        }
+        __syncthreads();
+        if (threadIdx.x < 64) {  // lane l owns bins 4l..4l+3; suffix sums from the top bin
+            const int l = threadIdx.x;
+            const uint32_t b0 = hist[4 * l], b1 = hist[4 * l + 1], b2 = hist[4 * l + 2],
+                           b3 = hist[4 * l + 3];
+            const uint32_t own = b0 + b1 + b2 + b3;
+            uint32_t above = own;  // inclusive suffix sum over lanes
+            for (int d = 1; d < 64; d <<= 1) {
+                const uint32_t o = __shfl_down(above, d);
+                if (l + d < 64) above += o;
+            }
+            above -= own;  // keys in higher lanes' bins
+            uint32_t c = above;
+            const uint32_t bins[4] = {b0, b1, b2, b3};
+            for (int j = 3; j >= 0; --j) {
+                if (c < (uint32_t)rest && c + bins[j] >= (uint32_t)rest) {
+                    hist[256] = 4 * l + j;
+                    hist[257] = c;
+                }
+                c += bins[j];
+            }
+        }
+        __syncthreads();
+        prefix |= hist[256] << shift;
+        rest -= (int)hist[257];
+        __syncthreads();
+    }
+    threshold = prefix;
+    ties = rest;
+}
+
+// Exclusive prefix sum over the workgroup of one small count per thread, and the total. `sums` is
+// LDS of one word per wave plus one.
+__device__ inline int block_prefix(int v, int* sums, int& total) {
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, waves = blockDim.x >> 6;
+    int inc = v;
+    for (int d = 1; d < 64; d <<= 1) {
+        const int o = __shfl_up(inc, d);
+        if (lane >= d) inc += o;
+    }
+    __syncthreads();  // the sums of an earlier call have been read
+    if (lane == 63) sums[wave] = inc;
+    __syncthreads();
+    int before = 0, all = 0;
+    for (int w = 0; w < waves; ++w) {
+        const int c = sums[w];
+        if (w < wave) before += c;
+        all += c;
+    }
+    total = all;
+    return before + inc - v;
+}
+
+}  // namespace sc
+
+#endif  // SHORTCONV_CACHE_DEVICE_H
