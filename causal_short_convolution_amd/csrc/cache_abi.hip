@@ -3,6 +3,7 @@
 #include <stdarg.h>
 #include <stdio.h>
 
+#include "cache_attention.h"
 #include "cache_internal.h"
 #include "shortconv_cache.h"
 
@@ -200,9 +201,22 @@ int verify_tree(const char* fn, bool mx, const void* k, const void* v, int64_t k
 // ------------------------------------------------------------------------------------------------
 enum Kind { TREE, BLOCKS, SCORES };
 
-size_t attention_workspace(Kind, int64_t, int32_t, int32_t, int32_t, int32_t, int32_t, int32_t,
-                           int32_t) {
-    return 0;
+// Query rows that share a unit: those of an average sequence, or of one token.
+int unit_row_tiles(Kind kind, int64_t tokens, int32_t num_seqs, int32_t q_heads, int32_t heads) {
+    const int64_t group = q_heads / heads;
+    const int64_t each = kind == TREE && num_seqs > 0 ? (tokens + num_seqs - 1) / num_seqs : 1;
+    return sc::row_tiles(each * group);
+}
+
+int64_t part_offset(int32_t num_seqs) { return ((int64_t)num_seqs + 1) * 8 / 256 * 256 + 256; }
+
+// The prefix sums of the sequences' steps (tree), and two parts per worker: rows of D sums, then
+// the rows' maxima and sums.
+size_t attention_workspace(Kind kind, int64_t tokens, int32_t num_seqs, int32_t q_heads,
+                           int32_t heads, int32_t D) {
+    const int R = unit_row_tiles(kind, tokens, num_seqs, q_heads, heads);
+    return part_offset(kind == TREE ? num_seqs : 0) +
+           (size_t)sc::workers(D) * 2 * 16 * R * (D + 2) * sizeof(float);
 }
 
 int attention(const char* fn, Kind kind, bool mx, const void* q, int64_t q_stride,
@@ -239,8 +253,9 @@ int attention(const char* fn, Kind kind, bool mx, const void* q, int64_t q_strid
     }
     const void* ptrs[] = {q, k, v, out, ws};
     SC_TRY(check_aligned(fn, ptrs, 5));
-    const size_t need = attention_workspace(kind, tokens, num_seqs, topk, block_size, q_heads,
-                                            heads, D, dtype);
+    const size_t need = kind == SCORES ? 0
+                                       : attention_workspace(kind, tokens, num_seqs, q_heads,
+                                                             heads, D);
     if (need > 0 && (!ws || ws_bytes < need))
         return fail(SC_ERR_INVALID, "%s: workspace of %zu bytes needed, %zu given", fn, need,
                     ws ? ws_bytes : (size_t)0);
@@ -263,13 +278,15 @@ int attention(const char* fn, Kind kind, bool mx, const void* q, int64_t q_strid
     a.scores_out = scores_out;
     a.capacity = capacity;
     a.ws = ws;
+    a.part_offset = part_offset(kind == TREE ? num_seqs : 0);
     a.heads = heads;
     a.group = q_heads / heads;
     a.scale = scale;
     const hipStream_t st = (hipStream_t)stream;
-    return launched(fn, kind == TREE     ? sc::launch_tree_attention(a, mx, dtype, D, st)
-                        : kind == BLOCKS ? sc::launch_block_attention(a, mx, dtype, D, st)
-                                         : sc::launch_cache_scores(a, mx, dtype, D, st));
+    if (kind == SCORES) return launched(fn, sc::launch_cache_scores(a, mx, dtype, D, st));
+    const int R = unit_row_tiles(kind, tokens, num_seqs, q_heads, heads);
+    return launched(fn, kind == TREE ? sc::launch_tree_attention(a, mx, dtype, D, R, st)
+                                     : sc::launch_block_attention(a, mx, dtype, D, R, st));
 }
 
 size_t bad_size(const char* fn, const char* why) {
@@ -439,8 +456,7 @@ SC_API size_t shortconv_tree_attention_workspace_size(int64_t total_tokens, int3
         return SIZE_MAX;
     if (total_tokens < 0 || total_tokens > INT32_MAX || num_seqs < 0)
         return bad_size(fn, "bad total_tokens or num_seqs");
-    return attention_workspace(TREE, total_tokens, num_seqs, 0, 1, num_q_heads, num_heads,
-                               head_dim, dtype);
+    return attention_workspace(TREE, total_tokens, num_seqs, num_q_heads, num_heads, head_dim);
 }
 
 SC_API int shortconv_block_summary(const void* k_cache, const int32_t* cu_seqlens,
@@ -565,8 +581,7 @@ SC_API size_t shortconv_block_attention_workspace_size(int64_t total_tokens, int
         return SIZE_MAX;
     if (total_tokens < 0 || total_tokens > INT32_MAX || topk < 0 || block_size < 1)
         return bad_size(fn, "bad total_tokens, topk or block_size");
-    return attention_workspace(BLOCKS, total_tokens, 0, topk, block_size, num_q_heads, num_heads,
-                               head_dim, dtype);
+    return attention_workspace(BLOCKS, total_tokens, 0, num_q_heads, num_heads, head_dim);
 }
 
 SC_API int shortconv_cache_scores(const void* q, int64_t q_tok_stride, const float* lse,

@@ -1,170 +1,644 @@
-// Attention over the paged cache (shortconv_tree_attention, shortconv_block_attention) and the sums
-// of its weights (shortconv_cache_scores).
-#include "cache_device.h"
+// Attention over the paged cache: shortconv_tree_attention (the new tokens of each sequence, a tree
+// or one token, over all its keys) and shortconv_block_attention (each new token over the pages
+// selected for it).
+//
+// The work is cut into units: a cache head of a sequence (of a token, for selected pages) with the
+// query rows that read it, up to 16 R of them, R = 1 or 2. A unit's keys are cut into steps of
+// 4 wave tiles. All steps of all units lie in one line that the workgroups share out evenly, each
+// taking a run of consecutive steps, so one long sequence among short ones, or few units with many
+// keys, still fill the chip; the lengths are read on the device, so a captured launch follows them.
+// In a step the 4 waves take different keys, each with its own running maximum and sum; at the end
+// of the unit they meet in LDS. A unit that ends inside one workgroup's run is written at once;
+// one that crosses workgroups leaves its unnormalized sums in the workspace, and a second launch
+// joins them (a fixed order: the same inputs give the same bits).
+#include "attention_tile.h"
+#include "cache_attention.h"
 
 namespace sc {
 namespace {
 
 constexpr int kBlock = 256;
+constexpr int kWaves = 4;
 
-// The lane's D / 64 consecutive channels of one head of a cache row, in fp32.
-template <class E, bool MX, int D>
-__device__ inline void load_head(const void* cache, const void* scales, int32_t slot, int heads,
-                                 int h, float (&f)[D / 64]) {
-    constexpr int N = D / 64;
-    const int64_t at = ((int64_t)slot * heads + h) * D + (threadIdx.x & 63) * N;
-#pragma unroll
-    for (int j = 0; j < N; ++j) {
-        if constexpr (MX) {
-            const uint8_t code = static_cast<const uint8_t*>(cache)[at + j];
-            const uint8_t e = static_cast<const uint8_t*>(scales)[at >> 5];
-            typedef float f32x2 __attribute__((ext_vector_type(2)));
-            const f32x2 w = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(
-                (uint32_t)code, __uint_as_float(e ? (uint32_t)e << 23 : 0x00400000u), false);
-            f[j] = w[0];
-        } else if constexpr (E::BYTES == 4) {
-            f[j] = static_cast<const float*>(cache)[at + j];
-        } else {
-            f[j] = __uint_as_float((uint32_t)static_cast<const uint16_t*>(cache)[at + j] << 16);
-        }
+// Step w of `total` steps over `workers` workers: worker i owns [share_begin(i), share_begin(i+1)).
+template <int WORKERS>
+struct Shares {
+    int64_t total, each, more;
+    int32_t workers;
+    __device__ Shares(int64_t t) : total(t) {
+        workers = (int32_t)(t < WORKERS ? t : WORKERS);
+        each = workers ? t / workers : 0;
+        more = workers ? t - each * workers : 0;
     }
+    __device__ int64_t begin(int32_t w) const { return w * each + (w < more ? w : more); }
+    __device__ int32_t owner(int64_t step) const {
+        const int64_t cut = more * (each + 1);
+        return (int32_t)(step < cut ? step / (each + 1) : more + (step - cut) / each);
+    }
+};
+
+// One unit of work and its query rows.
+struct Unit {
+    int32_t s;          // sequence
+    int32_t h;          // cache head
+    int32_t row0;       // first query row (of the sequence's len * group, or the token's group)
+    int32_t rows;       // rows in this unit, 1 .. 16 R
+    int32_t steps;      // steps of all its keys, at least 1
+    int64_t tok;        // selected pages: the token
+    int64_t first;      // its first step in the line
+};
+
+template <class E, bool MX, int D, int R, bool SPARSE>
+struct Geometry {
+    using T = Tile<E, MX, D>;
+    static constexpr int M = 16 * R;
+    static constexpr int KW = 16 * T::SUB;        // keys per wave and step
+    static constexpr int KS = KW * kWaves;        // keys per step
+    __device__ static inline int64_t key_steps(int64_t keys) {
+        return keys > KS ? (keys + KS - 1) / KS : 1;
+    }
+    // Steps of a sequence: its cache heads, times its row tiles, times its key steps.
+    __device__ static inline int64_t seq_steps(const AttnArgs& a, const SeqInfo& q) {
+        if (q.len == 0) return 0;
+        const int64_t tiles = ((int64_t)q.len * a.group + M - 1) / M;
+        return a.heads * tiles * key_steps(q.keys);
+    }
+    __device__ static inline int32_t block_steps(const AttnArgs& a) {
+        return (int32_t)key_steps((int64_t)a.topk << a.pg.shift);
+    }
+    __device__ static inline int32_t group_tiles(const AttnArgs& a) {
+        return (a.group + M - 1) / M;
+    }
+};
+
+// 32 mask bits of a row from bit `at` on; bits before 0 are the cached keys (ones).
+__device__ inline uint32_t mask_bits(const AttnArgs& a, int64_t t, int32_t i, int32_t at) {
+    if (at <= -32) return 0xffffffffu;
+    if (a.mask == nullptr) {
+        const int32_t n = i - at + 1;  // new tokens 0..i, and the cached keys before them
+        return n >= 32 ? 0xffffffffu : n <= 0 ? 0u : (1u << n) - 1u;
+    }
+    const uint64_t* m = reinterpret_cast<const uint64_t*>(a.mask) + t * a.words;
+    if (at < 0) {
+        const uint64_t w = a.words > 0 ? m[0] : 0;
+        return (uint32_t)(w << -at) | ((1u << -at) - 1u);
+    }
+    const int32_t j = at >> 6, sh = at & 63;
+    const uint64_t lo = j < a.words ? m[j] : 0;
+    const uint64_t hi = j + 1 < a.words ? m[j + 1] : 0;
+    return (uint32_t)(sh ? (lo >> sh) | (hi << (64 - sh)) : lo);
 }
 
-__device__ inline bool looks_at(const AttnArgs& a, int64_t t, int32_t i, int32_t j) {
-    if (a.mask == nullptr) return j <= i;
-    if ((j >> 6) >= a.words) return false;
-    return (a.mask[t * a.words + (j >> 6)] >> (j & 63)) & 1;
-}
+template <class E, bool MX, int D, int R, bool SPARSE, bool PAGE16>
+__global__ void __launch_bounds__(kBlock, workers_per_cu(D)) attention_kernel(AttnArgs a) {
+    using G = Geometry<E, MX, D, R, SPARSE>;
+    using T = Tile<E, MX, D>;
+    constexpr int kWorkers = workers(D);
+    constexpr int M = G::M;
+    constexpr int KW = G::KW;
+    constexpr int SUB = T::SUB;
+    constexpr uint32_t kFull = SUB == 2 ? 0xffffffffu : 0xffffu;
+    constexpr int QSTRIDE = D * T::QB + 16;  // query rows in LDS, staggered over the banks
+    constexpr bool QREG = R == 1 && D <= 128;  // query operands stay in registers
+    constexpr int OSTRIDE = D + 4;           // output rows in LDS (floats)
+    constexpr int kLds = 2 * M * OSTRIDE * 4 > M * QSTRIDE ? 2 * M * OSTRIDE * 4 : M * QSTRIDE;
+    __shared__ __attribute__((aligned(16))) char lds[kLds];
+    __shared__ float stat[kWaves][2][M];
+    __shared__ int64_t sums[kWaves];
+    __shared__ int32_t found_s;
+    __shared__ int64_t found_first;
+    __shared__ int32_t left_out_any;
 
-// One wave per (token, query head): keys one after the other with a running maximum and sum.
-template <class E, bool MX, int D, bool SPARSE>
-__global__ void __launch_bounds__(kBlock) attention_kernel(AttnArgs a) {
-    constexpr int N = D / 64;
-    const int64_t t = blockIdx.x;
-    const int hq = uniform((int)(blockIdx.y * 4 + (threadIdx.x >> 6)));
-    const int s = seq_of_token(a.b, t);
-    const SeqInfo sq = seq_info(a.b, a.pg, s);
-    const int64_t i64 = t - sq.start;
-    if (i64 < 0 || i64 >= sq.len || hq >= a.heads * a.group) return;
-    const int32_t i = (int32_t)i64;
-    const int h = hq / a.group;
-    float q[N], o[N];
-    load_head<E, false, D>(static_cast<const char*>(a.q) + t * a.q_stride * E::BYTES, nullptr, 0,
-                           a.heads * a.group, hq, q);
-    for (int j = 0; j < N; ++j) o[j] = 0.0f;
-    float m = -__builtin_inff(), l = 0.0f;
-    auto key = [&](int32_t p) {
-        const int32_t slot = slot_of(a.pg, s, p);
-        if (slot < 0) return;
-        float k[N], v[N];
-        load_head<E, MX, D>(a.cache[0], a.scales[0], slot, a.heads, h, k);
-        load_head<E, MX, D>(a.cache[1], a.scales[1], slot, a.heads, h, v);
-        float x = 0.0f;
-        for (int j = 0; j < N; ++j) x = __builtin_fmaf(q[j], k[j], x);
-        x = head_sum<64>(x) * a.scale;
-        const float top = __builtin_fmaxf(m, x);
-        if (top == -__builtin_inff()) return;
-        const float old = __expf(m - top), w = __expf(x - top);
-        l = l * old + w;
-        for (int j = 0; j < N; ++j) o[j] = __builtin_fmaf(w, v[j], o[j] * old);
-        m = top;
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int wave = uniform(tid >> 6);
+    const int c = lane & 15, g = lane >> 4;
+    // Workgroups go round the 8 XCDs by blockIdx. Where every worker has steps, consecutive runs
+    // go to one XCD, so that units that read the same rows meet in its L2; fewer steps than
+    // workers are spread over the XCDs.
+    auto worker = [&](int64_t steps) {
+        return steps < kWorkers ? (int32_t)blockIdx.x
+                                : (int32_t)(blockIdx.x & 7) * (kWorkers / 8) +
+                                      (int32_t)(blockIdx.x >> 3);
     };
+    const int eb = MX ? 1 : E::BYTES;
+    const uint32_t row_bytes = (uint32_t)(a.heads * D * eb);
+    char* ws = static_cast<char*>(a.ws);
+
+    // ---- this worker's run of steps, and the unit it begins in
+    int64_t total, at, end;
+    Unit u;
     if constexpr (SPARSE) {
-        const int32_t last = min((int64_t)sq.keys - 1, (int64_t)sq.ctx + i);
-        for (int c = 0; c < a.topk; ++c) {
-            const int32_t pb = a.selected[(t * a.heads + h) * a.topk + c];
-            if (pb < 0 || pb >= a.pg.max_blocks) continue;
-            for (int r = 0; r < (1 << a.pg.shift); ++r) {
-                const int32_t p = (pb << a.pg.shift) + r;
-                if (p <= last) key(p);
+        u.steps = G::block_steps(a);
+        total = a.b.tokens * a.heads * G::group_tiles(a) * u.steps;
+    } else {
+        const int per = (a.b.num_seqs + kBlock - 1) / kBlock;
+        int64_t mine = 0;
+        for (int j = 0; j < per; ++j) {
+            const int s = tid * per + j;
+            if (s < a.b.num_seqs) mine += G::seq_steps(a, seq_info(a.b, a.pg, s));
+        }
+        int64_t inc = mine;
+        for (int d = 1; d < 64; d <<= 1) {
+            const int64_t o = __shfl_up(inc, d);
+            if (lane >= d) inc += o;
+        }
+        if (lane == 63) sums[wave] = inc;
+        __syncthreads();
+        int64_t before = 0;
+        total = 0;
+        for (int w = 0; w < kWaves; ++w) {
+            if (w < wave) before += sums[w];
+            total += sums[w];
+        }
+        const Shares<kWorkers> sh(total);
+        const int32_t me = worker(total);
+        const int64_t want = me < sh.workers ? sh.begin(me) : -1;
+        int64_t x = before + inc - mine;
+        int64_t* prefix = reinterpret_cast<int64_t*>(ws);
+        for (int j = 0; j < per; ++j) {
+            const int s = tid * per + j;
+            if (s >= a.b.num_seqs) break;
+            const int64_t n = G::seq_steps(a, seq_info(a.b, a.pg, s));
+            if (want >= x && want < x + n) {
+                found_s = s;
+                found_first = x;
+            }
+            if (me == 0) prefix[s] = x;
+            x += n;
+        }
+        if (me == 0 && tid == kBlock - 1) prefix[a.b.num_seqs] = total;
+        __syncthreads();
+    }
+    const Shares<kWorkers> sh(total);
+    const int32_t me = worker(total);
+    if (me >= sh.workers) return;
+    at = sh.begin(me);
+    end = sh.begin(me + 1);
+    SeqInfo q;
+    int32_t tiles;
+    int64_t seq_first = 0;
+    if constexpr (!SPARSE) {
+        u.s = uniform(found_s);
+        seq_first = uniform(found_first);
+        q = seq_info(a.b, a.pg, u.s);
+    }
+
+    while (at < end) {
+        // ---- the unit that step `at` belongs to
+        int64_t tok = 0;   // first token of its rows
+        int32_t last = 0;  // selected pages: the token's own position
+        bool real = true;
+        if constexpr (SPARSE) {
+            tiles = G::group_tiles(a);
+            const int64_t n = at / u.steps;
+            u.first = n * u.steps;
+            const int32_t tile = (int32_t)(n % tiles);
+            const int64_t th = n / tiles;
+            u.h = (int32_t)(th % a.heads);
+            u.tok = th / a.heads;
+            u.s = seq_of_token(a.b, u.tok);
+            q = seq_info(a.b, a.pg, u.s);
+            tok = u.tok;
+            const int64_t i = tok - q.start;
+            real = i >= 0 && i < q.len;  // a token behind the last sequence has no output
+            last = (int32_t)min((int64_t)(a.pg.max_blocks << a.pg.shift) - 1, (int64_t)q.ctx + i);
+            u.row0 = tile * M;
+            u.rows = min(M, a.group - u.row0);
+        } else {
+            while (at >= seq_first + G::seq_steps(a, q)) {  // on to the next sequence
+                seq_first += G::seq_steps(a, q);
+                ++u.s;
+                q = seq_info(a.b, a.pg, u.s);
+            }
+            u.steps = (int32_t)G::key_steps(q.keys);
+            const int64_t rows = (int64_t)q.len * a.group;
+            tiles = (int32_t)((rows + M - 1) / M);
+            const int64_t n = (at - seq_first) / u.steps;
+            u.first = seq_first + n * u.steps;
+            u.h = (int32_t)(n / tiles);
+            const int64_t r0 = (n % tiles) * M;
+            u.row0 = (int32_t)r0;
+            u.rows = (int32_t)(rows - r0 < M ? rows - r0 : M);
+            tok = q.start;
+        }
+        const int32_t step0 = (int32_t)(at - u.first);
+        const int64_t unit_end = u.first + u.steps;
+        const int32_t step1 = (int32_t)((end < unit_end ? end : unit_end) - u.first);
+        at = u.first + step1;
+        if (!real) continue;
+
+        // Query row r of the unit: token and query head (rows past the last repeat it).
+        auto row_token = [&](int r) {
+            const int32_t x = u.row0 + (r < u.rows ? r : u.rows - 1);
+            return SPARSE ? tok : tok + x / a.group;
+        };
+        auto row_head = [&](int r) {
+            const int32_t x = u.row0 + (r < u.rows ? r : u.rows - 1);
+            return u.h * a.group + (SPARSE ? x : x % a.group);
+        };
+        // ---- queries: to LDS, whole rows
+        __syncthreads();  // the last unit's use of LDS is over
+        if (tid == 0) left_out_any = 0;
+        {
+            constexpr int PIECES = D * T::QB / 16;
+            const char* qb = static_cast<const char*>(a.q);
+            for (int x = tid; x < M * PIECES; x += kBlock) {
+                const int r = x / PIECES, p = x % PIECES;
+                const int64_t off = row_token(r) * a.q_stride + (int64_t)row_head(r) * D;
+                *reinterpret_cast<uint4*>(lds + r * QSTRIDE + p * 16) =
+                    *reinterpret_cast<const uint4*>(qb + off * T::QB + p * 16);
             }
         }
-    } else {
-        for (int32_t p = 0; p < sq.keys; ++p)
-            if (p < sq.ctx || looks_at(a, t, i, p - sq.ctx)) key(p);
-    }
-    const float inv = l > 0.0f || l != l ? 1.0f / l : 0.0f;
-    const int64_t at = (t * a.heads * a.group + hq) * D + (threadIdx.x & 63) * N;
-    for (int j = 0; j < N; ++j) {
-        const float y = o[j] * inv;
-        if constexpr (E::BYTES == 4) static_cast<float*>(a.out)[at + j] = y;
-        else static_cast<__bf16*>(a.out)[at + j] = (__bf16)y;
-    }
-    if (a.lse != nullptr && (threadIdx.x & 63) == 0)
-        a.lse[t * a.heads * a.group + hq] = l > 0.0f || l != l ? m + __logf(l) : -__builtin_inff();
-}
+        __syncthreads();
+        typename T::Q qreg;
+        if constexpr (QREG) T::load_q(lds + c * QSTRIDE, g, qreg);
 
-// One wave per (sequence, head, key), over the rows that look at it.
-template <class E, bool MX, int D>
-__global__ void __launch_bounds__(kBlock) scores_kernel(AttnArgs a) {
-    constexpr int N = D / 64;
-    const int h = blockIdx.y, s = blockIdx.z;
-    const SeqInfo sq = seq_info(a.b, a.pg, s);
-    const int64_t row = ((int64_t)s * a.heads + h) * a.capacity;
-    for (int64_t p64 = blockIdx.x * 4 + (threadIdx.x >> 6); p64 < sq.keys && p64 < a.capacity;
-         p64 += gridDim.x * 4) {
-        const int32_t p = uniform((int32_t)p64);
-        const int32_t slot = slot_of(a.pg, s, p);
-        float sum = a.scores_in != nullptr && p < sq.ctx ? a.scores_in[row + p] : 0.0f;
-        if (slot >= 0) {
-            float k[N], q[N];
-            load_head<E, MX, D>(a.cache[0], a.scales[0], slot, a.heads, h, k);
-            for (int32_t i = 0; i < sq.len; ++i) {
-                const int64_t t = sq.start + i;
-                if (p >= sq.ctx && !looks_at(a, t, i, p - sq.ctx)) continue;
-                for (int g = 0; g < a.group; ++g) {
-                    const int hq = h * a.group + g;
-                    load_head<E, false, D>(static_cast<const char*>(a.q) + t * a.q_stride * E::BYTES,
-                                           nullptr, 0, a.heads * a.group, hq, q);
-                    float x = 0.0f;
-                    for (int j = 0; j < N; ++j) x = __builtin_fmaf(q[j], k[j], x);
-                    x = head_sum<64>(x) * a.scale;
-                    const float z = a.lse[t * a.heads * a.group + hq];
-                    if (z != -__builtin_inff()) sum += __expf(x - z);
+        // ---- the wave's keys of one step
+        const char* kc = static_cast<const char*>(a.cache[0]) + (int64_t)u.h * D * eb;
+        const char* vc = static_cast<const char*>(a.cache[1]) + (int64_t)u.h * D * eb;
+        const char* ks = static_cast<const char*>(a.scales[0]) + u.h * (D / 32);
+        const char* vs = static_cast<const char*>(a.scales[1]) + u.h * (D / 32);
+        const int32_t* table = a.pg.table + (int64_t)u.s * a.pg.max_blocks;
+        const int32_t* sel = SPARSE ? a.selected + (tok * a.heads + u.h) * a.topk : nullptr;
+        // The row of flattened key kk (16 of them with PAGE16) and how many keys exist from there.
+        auto find = [&](int32_t kk, int32_t& exist) -> int32_t {
+            int32_t pos = kk;
+            int32_t limit = q.keys - 1;
+            exist = 0;
+            if constexpr (SPARSE) {
+                const int32_t n = kk >> a.pg.shift;
+                if (n >= a.topk) return 0;
+                const int32_t pb = sel[n];
+                if (pb < 0 || pb >= a.pg.max_blocks) return 0;
+                pos = (pb << a.pg.shift) + (kk & ((1 << a.pg.shift) - 1));
+                limit = last;
+            }
+            if (pos > limit) return 0;
+            const int32_t page = table[pos >> a.pg.shift];
+            if (page < 0 || page >= a.pg.num_pages) return 0;
+            exist = limit - pos + 1;
+            return (page << a.pg.shift) + (pos & ((1 << a.pg.shift) - 1));
+        };
+        using KT = KeyTile<SUB, PAGE16>;
+        auto locate = [&](int32_t step) {
+            KT t;
+            const int32_t k0 = step * G::KS + wave * KW;
+            t.valid = 0;
+            if constexpr (PAGE16) {
+#pragma unroll
+                for (int s = 0; s < SUB; ++s) {
+                    int32_t exist;
+                    t.base[s] = uniform(find(k0 + s * 16, exist));
+                    exist = uniform(exist);
+                    const uint32_t bits = exist >= 16 ? 0xffffu : (1u << exist) - 1u;
+                    t.valid |= bits << (16 * s);
+                }
+                if (SUB == 2) {  // a subtile without keys reads the other one's rows
+                    if (!(t.valid & 0xffffu)) t.base[0] = t.base[SUB - 1];
+                    if (!(t.valid >> 16)) t.base[SUB - 1] = t.base[0];
+                }
+            } else {
+                int32_t exist;
+                t.base[0] = find(k0 + (lane & (KW - 1)), exist);
+                t.valid = (uint32_t)__ballot(exist > 0) & kFull;
+            }
+            return t;
+        };
+
+        float m[R], l[R];
+        f32x4 acc[R][T::NT];
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            m[r] = -__builtin_inff();
+            l[r] = 0.0f;
+#pragma unroll
+            for (int i = 0; i < T::NT; ++i) acc[r][i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+        }
+        const float to_log2 = a.scale * kLog2e;
+        typename T::K kreg;
+        typename T::V vreg;
+        auto next_tile = [&](int32_t& step, KT& t) {  // the next step from `step` on with a key
+            for (; step < step1; ++step) {
+                t = locate(step);
+                if (t.valid) return true;
+            }
+            return false;
+        };
+        int32_t left_out = 0;
+        int32_t step = step0;
+        KT tile;
+        bool more = next_tile(step, tile);
+        if (more) {
+            T::load_k(kc, ks, tile, row_bytes, c, g, kreg);
+            T::load_v(vc, vs, tile, row_bytes, c, g, vreg);
+        }
+        // Per step: logits from K, then the loads of the next K into the same registers, softmax
+        // and the product with V, then the loads of the next V.
+        while (more) {
+            if constexpr (!QREG) asm volatile("" ::: "memory");  // queries are read anew from LDS
+            const int32_t k0 = step * G::KS + wave * KW;
+            const uint32_t valid = tile.valid;
+            f32x4 x[R][SUB];
+#pragma unroll
+            for (int s = 0; s < SUB; ++s) {
+                typename T::KOp ko;
+                T::k_operands(kreg, s, g, ko);
+#pragma unroll
+                for (int r = 0; r < R; ++r) {
+                    if constexpr (QREG) {
+                        x[r][s] = T::logits(ko, qreg);
+                    } else {
+                        typename T::Q qr;
+                        T::load_q(lds + (r * 16 + c) * QSTRIDE, g, qr);
+                        x[r][s] = T::logits(ko, qr);
+                    }
                 }
             }
+            KT next;
+            int32_t next_step = step + 1;
+            const bool another = next_tile(next_step, next);
+            if (another) T::load_k(kc, ks, next, row_bytes, c, g, kreg);
+
+            // Which keys a row looks at. Every key of a full step below the context is seen by all
+            // rows; selected pages are one token's, seen alike by all its heads.
+            const bool all_seen = valid == kFull && (SPARSE || k0 + KW <= q.ctx);
+            typename T::VOp vo;
+            T::v_operands(vreg, vo);
+            if (!all_seen) {
+                // Keys that do not exist have rows that hold anything. Among the new tokens a row
+                // of V may be one that only some query rows look at, and an infinity or a NaN
+                // times a weight of zero would reach the others: those elements are left out
+                // here and added at the end of the unit to the rows that do look at them.
+                if (valid != kFull) T::clear(vo, valid, g);
+                if (!SPARSE && T::cleanse(vo)) left_out = 1;
+            }
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+                float p[SUB * 4];
+                float top = m[r];
+                uint32_t bits = valid;
+                if (!SPARSE && !all_seen) {
+                    const int64_t t = row_token(r * 16 + c);
+                    bits &= mask_bits(a, t, (int32_t)(t - q.start), k0 - q.ctx);
+                }
+#pragma unroll
+                for (int j = 0; j < SUB * 4; ++j) {
+                    p[j] = x[r][j >> 2][j & 3] * to_log2;
+                    if (!all_seen) {
+                        const bool see = (bits >> ((j >> 2) * 16 + g * 4 + (j & 3))) & 1;
+                        p[j] = see ? p[j] : -__builtin_inff();
+                    }
+                    top = __builtin_fmaxf(top, p[j]);
+                }
+                top = row_max(top);
+                if (__ballot(top > m[r])) {  // rescale only when a maximum of the tile has moved
+                    const float base = top == -__builtin_inff() ? 0.0f : top;
+                    const float f = exp2_fast(m[r] - base);
+                    l[r] *= f;
+#pragma unroll
+                    for (int i = 0; i < T::NT; ++i)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) acc[r][i][e] *= f;
+                    m[r] = top;
+                }
+                const float base = m[r] == -__builtin_inff() ? 0.0f : m[r];
+#pragma unroll
+                for (int j = 0; j < SUB * 4; ++j) {
+                    p[j] = exp2_fast(p[j] - base);
+                    l[r] += p[j];
+                }
+                T::values(vo, p, acc[r]);
+            }
+            if (another) T::load_v(vc, vs, next, row_bytes, c, g, vreg);
+            more = another;
+            step = next_step;
+            tile = next;
         }
-        if ((threadIdx.x & 63) == 0) a.scores_out[row + p] = sum;
+
+        // ---- the four waves meet: common maximum, then the sums in a fixed order
+        __syncthreads();  // every wave is done with the queries in LDS
+        float big[R], sum[R];
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            l[r] = row_sum(l[r]);
+            if (g == 0) {
+                stat[wave][0][r * 16 + c] = m[r];
+                stat[wave][1][r * 16 + c] = l[r];
+            }
+        }
+        if (left_out) left_out_any = 1;
+        __syncthreads();
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            big[r] = -__builtin_inff();
+            for (int w = 0; w < kWaves; ++w)
+                big[r] = __builtin_fmaxf(big[r], stat[w][0][r * 16 + c]);
+            const float base = big[r] == -__builtin_inff() ? 0.0f : big[r];
+            sum[r] = 0.0f;
+            for (int w = 0; w < kWaves; ++w)
+                sum[r] += stat[w][1][r * 16 + c] * exp2_fast(stat[w][0][r * 16 + c] - base);
+            const float f = exp2_fast(m[r] - base);
+#pragma unroll
+            for (int i = 0; i < T::NT; ++i)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) acc[r][i][e] *= f;
+        }
+        float* buf = reinterpret_cast<float*>(lds);
+        auto exchange = [&](int half, bool put) {
+#pragma unroll
+            for (int r = 0; r < R; ++r)
+#pragma unroll
+                for (int v = 0; v < T::NU; ++v)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+#pragma unroll
+                        for (int e = 0; e < T::CH; e += 4) {
+                            f32x4* at_ = reinterpret_cast<f32x4*>(
+                                buf + (half * M + r * 16 + c) * OSTRIDE + v * 16 * T::CH +
+                                (g * 4 + i) * T::CH + e);
+                            const int n = v * T::CH + e;
+                            if (put) {
+                                *at_ = f32x4{acc[r][n][i], acc[r][n + 1][i], acc[r][n + 2][i],
+                                             acc[r][n + 3][i]};
+                            } else {
+                                const f32x4 y = *at_;
+#pragma unroll
+                                for (int k = 0; k < 4; ++k) acc[r][n + k][i] += y[k];
+                            }
+                        }
+        };
+        if (wave >= 2) exchange(wave - 2, true);
+        __syncthreads();
+        if (wave < 2) exchange(wave, false);
+        __syncthreads();
+        if (wave == 1) exchange(0, true);
+        __syncthreads();
+        // Adds the infinities and NaN that the row's channels d.. have in the new tokens it looks at
+        // (of this part's steps) and that the products left out.
+        auto add_left_out = [&](int row, int d, float (&y)[T::CH]) {
+            const int64_t t = row_token(row);
+            const int32_t k1 = min((int64_t)q.keys, (int64_t)step1 * G::KS);
+            for (int32_t k = max(q.ctx, step0 * G::KS); k < k1; ++k) {
+                if (!(mask_bits(a, t, (int32_t)(t - q.start), k - q.ctx) & 1)) continue;
+                const int32_t slot = slot_of(a.pg, u.s, k);
+                if (slot < 0) continue;
+                const int64_t e0 = ((int64_t)slot * a.heads + u.h) * D + d;
+                for (int e = 0; e < T::CH; ++e) {
+                    const float f = cache_element<E, MX>(a.cache[1], a.scales[1], e0 + e);
+                    if ((__float_as_uint(f) & 0x7f800000u) == 0x7f800000u) y[e] += f;
+                }
+            }
+        };
+        if (wave == 0) {
+            exchange(0, false);
+            const bool whole = step0 == 0 && step1 == u.steps;
+            // A part of a unit: slot 1 if it holds the unit's first step (the worker's last
+            // part), else slot 0 (its first).
+            float* part = reinterpret_cast<float*>(ws + a.part_offset) +
+                          ((int64_t)me * 2 + (step0 == 0 ? 1 : 0)) * (M * (D + 2));
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+                const int row = r * 16 + c;
+                const bool some = sum[r] > 0.0f || sum[r] != sum[r];
+                const float inv = whole ? (some ? 1.0f / sum[r] : 0.0f) : 1.0f;
+                if (!whole) {
+                    if (g == 0) {
+                        part[M * D + row] = big[r];
+                        part[M * D + M + row] = sum[r];
+                    }
+                } else if (row < u.rows && g == 0 && a.lse != nullptr) {
+                    a.lse[row_token(row) * a.heads * a.group + row_head(row)] =
+                        some ? (big[r] + log2_fast(sum[r])) * kLn2 : -__builtin_inff();
+                }
+                if (row >= u.rows) continue;
+                const int64_t o = (row_token(row) * a.heads * a.group + row_head(row)) * D;
+#pragma unroll
+                for (int v = 0; v < T::NU; ++v)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const int d = v * 16 * T::CH + (g * 4 + i) * T::CH;
+                        float y[T::CH];
+#pragma unroll
+                        for (int e = 0; e < T::CH; ++e) y[e] = acc[r][v * T::CH + e][i] * inv;
+                        if (!SPARSE && left_out_any) add_left_out(row, d, y);
+                        if (whole) {
+                            store_row<E, T::CH>(a.out, o + d, y);
+                        } else {
+#pragma unroll
+                            for (int e = 0; e < T::CH; e += 4)
+                                *reinterpret_cast<f32x4*>(part + row * D + d + e) =
+                                    f32x4{y[e], y[e + 1], y[e + 2], y[e + 3]};
+                        }
+                    }
+            }
+        }
     }
 }
 
-template <class E, bool MX, int D>
-hipError_t run(const AttnArgs& a, int what, hipStream_t st) {
-    if (what == 2) {
-        const int64_t keys = (int64_t)a.pg.max_blocks << a.pg.shift;
-        const uint32_t x = (uint32_t)(keys < 4096 ? (keys + 3) / 4 : 1024);
-        scores_kernel<E, MX, D><<<dim3(x, a.heads, a.b.num_seqs), kBlock, 0, st>>>(a);
+// Joins the parts of the units that crossed workers: one wave per (token, query head).
+template <class E, bool MX, int D, int R, bool SPARSE>
+__global__ void __launch_bounds__(kBlock) join_kernel(AttnArgs a) {
+    using G = Geometry<E, MX, D, R, SPARSE>;
+    constexpr int kWorkers = workers(D);
+    constexpr int M = G::M;
+    constexpr int N = D / 64;
+    const int lane = threadIdx.x & 63;
+    const int64_t t = blockIdx.x;
+    const int hq = uniform((int)(blockIdx.y * kWaves + (threadIdx.x >> 6)));
+    if (hq >= a.heads * a.group) return;
+    const int s = seq_of_token(a.b, t);
+    const SeqInfo q = seq_info(a.b, a.pg, s);
+    const int64_t i = t - q.start;
+    if (i < 0 || i >= q.len) return;
+    const char* ws = static_cast<const char*>(a.ws);
+    const int h = hq / a.group;
+    int64_t first, total;
+    int32_t steps, row;
+    if constexpr (SPARSE) {
+        steps = G::block_steps(a);
+        const int32_t tiles = G::group_tiles(a);
+        row = hq - h * a.group;
+        first = ((t * a.heads + h) * tiles + row / M) * steps;
+        total = a.b.tokens * a.heads * tiles * steps;
     } else {
-        const dim3 grid((uint32_t)a.b.tokens, (uint32_t)(a.heads * a.group + 3) / 4);
-        if (what == 1) attention_kernel<E, MX, D, true><<<grid, kBlock, 0, st>>>(a);
-        else attention_kernel<E, MX, D, false><<<grid, kBlock, 0, st>>>(a);
+        const int64_t* prefix = reinterpret_cast<const int64_t*>(ws);
+        steps = (int32_t)G::key_steps(q.keys);
+        const int64_t tiles = ((int64_t)q.len * a.group + M - 1) / M;
+        row = (int32_t)(i * a.group + hq - h * a.group);
+        first = prefix[s] + (h * tiles + row / M) * steps;
+        total = prefix[a.b.num_seqs];
     }
+    row %= M;
+    const Shares<kWorkers> sh(total);
+    const int32_t w0 = sh.owner(first), w1 = sh.owner(first + steps - 1);
+    if (w0 == w1) return;  // written by its worker
+    const float* parts = reinterpret_cast<const float*>(ws + a.part_offset);
+    auto part = [&](int32_t w) {
+        return parts + ((int64_t)w * 2 + (w == w0 ? 1 : 0)) * (M * (D + 2));
+    };
+    float big = -__builtin_inff();
+    for (int32_t w = w0; w <= w1; ++w) big = __builtin_fmaxf(big, part(w)[M * D + row]);
+    const float base = big == -__builtin_inff() ? 0.0f : big;
+    float sum = 0.0f, o[N];
+#pragma unroll
+    for (int j = 0; j < N; ++j) o[j] = 0.0f;
+    for (int32_t w = w0; w <= w1; ++w) {
+        const float* p = part(w);
+        const float f = exp2_fast(p[M * D + row] - base);
+        sum += p[M * D + M + row] * f;
+#pragma unroll
+        for (int j = 0; j < N; ++j)
+            o[j] = __builtin_fmaf(p[row * D + lane * N + j], f, o[j]);
+    }
+    const bool some = sum > 0.0f || sum != sum;
+    const float inv = some ? 1.0f / sum : 0.0f;
+#pragma unroll
+    for (int j = 0; j < N; ++j) o[j] *= inv;
+    const int64_t at = t * a.heads * a.group + hq;
+    store_row<E, N>(a.out, at * D + lane * N, o);
+    if (a.lse != nullptr && lane == 0)
+        a.lse[at] = some ? (big + log2_fast(sum)) * kLn2 : -__builtin_inff();
+}
+
+template <class E, bool MX, int D, int R, bool SPARSE>
+hipError_t run(const AttnArgs& a, hipStream_t st) {
+    if (a.pg.shift >= 4) attention_kernel<E, MX, D, R, SPARSE, true><<<workers(D), kBlock, 0, st>>>(a);
+    else attention_kernel<E, MX, D, R, SPARSE, false><<<workers(D), kBlock, 0, st>>>(a);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    const dim3 grid((uint32_t)a.b.tokens, (uint32_t)(a.heads * a.group + kWaves - 1) / kWaves);
+    join_kernel<E, MX, D, R, SPARSE><<<grid, kBlock, 0, st>>>(a);
     return hipGetLastError();
 }
 
-template <class E, bool MX>
-hipError_t by_dim(const AttnArgs& a, int what, int D, hipStream_t st) {
-    if (D == 64) return run<E, MX, 64>(a, what, st);
-    if (D == 128) return run<E, MX, 128>(a, what, st);
-    return run<E, MX, 256>(a, what, st);
+template <class E, bool MX, int D, bool SPARSE>
+hipError_t by_rows(const AttnArgs& a, int R, hipStream_t st) {
+    return R == 1 ? run<E, MX, D, 1, SPARSE>(a, st) : run<E, MX, D, 2, SPARSE>(a, st);
 }
 
-hipError_t dispatch(const AttnArgs& a, int what, bool mx, int dtype, int D, hipStream_t st) {
+template <class E, bool MX, bool SPARSE>
+hipError_t by_dim(const AttnArgs& a, int D, int R, hipStream_t st) {
+    if (D == 64) return by_rows<E, MX, 64, SPARSE>(a, R, st);
+    if (D == 128) return by_rows<E, MX, 128, SPARSE>(a, R, st);
+    return by_rows<E, MX, 256, SPARSE>(a, R, st);
+}
+
+template <bool SPARSE>
+hipError_t dispatch(const AttnArgs& a, bool mx, int dtype, int D, int R, hipStream_t st) {
     if (dtype == 0)
-        return mx ? by_dim<F32, true>(a, what, D, st) : by_dim<F32, false>(a, what, D, st);
-    return mx ? by_dim<BF16, true>(a, what, D, st) : by_dim<BF16, false>(a, what, D, st);
+        return mx ? by_dim<F32, true, SPARSE>(a, D, R, st) : by_dim<F32, false, SPARSE>(a, D, R, st);
+    return mx ? by_dim<BF16, true, SPARSE>(a, D, R, st) : by_dim<BF16, false, SPARSE>(a, D, R, st);
 }
 
 }  // namespace
 
-hipError_t launch_tree_attention(const AttnArgs& a, bool mx, int dtype, int D, hipStream_t st) {
-    return dispatch(a, 0, mx, dtype, D, st);
+hipError_t launch_tree_attention(const AttnArgs& a, bool mx, int dtype, int D, int R,
+                                 hipStream_t st) {
+    return dispatch<false>(a, mx, dtype, D, R, st);
 }
-hipError_t launch_block_attention(const AttnArgs& a, bool mx, int dtype, int D, hipStream_t st) {
-    return dispatch(a, 1, mx, dtype, D, st);
-}
-hipError_t launch_cache_scores(const AttnArgs& a, bool mx, int dtype, int D, hipStream_t st) {
-    return dispatch(a, 2, mx, dtype, D, st);
+hipError_t launch_block_attention(const AttnArgs& a, bool mx, int dtype, int D, int R,
+                                  hipStream_t st) {
+    return dispatch<true>(a, mx, dtype, D, R, st);
 }
 
 }  // namespace sc

@@ -72,6 +72,34 @@ __device__ inline uint32_t head_max(uint32_t v) {
     return v;
 }
 
+// N values to consecutive elements of type E, rounded once, in the widest stores that fit.
+template <class E, int N>
+__device__ inline void store_row(void* out, int64_t at, const float (&y)[N]) {
+    if constexpr (E::BYTES == 4) {
+        float* o = static_cast<float*>(out) + at;
+        if constexpr (N % 4 == 0) {
+#pragma unroll
+            for (int j = 0; j < N; j += 4)
+                *reinterpret_cast<float4*>(o + j) = make_float4(y[j], y[j + 1], y[j + 2], y[j + 3]);
+        } else {
+#pragma unroll
+            for (int j = 0; j < N; ++j) o[j] = y[j];
+        }
+    } else {
+        uint16_t* o = static_cast<uint16_t*>(out) + at;
+        if constexpr (N == 1) {
+            *reinterpret_cast<__bf16*>(o) = (__bf16)y[0];
+        } else if constexpr (N == 2) {
+            *reinterpret_cast<uint32_t*>(o) = BF16::pack2(y[0], y[1]);
+        } else if constexpr (N == 4) {
+            *reinterpret_cast<uint2*>(o) = make_uint2(BF16::pack2(y[0], y[1]), BF16::pack2(y[2], y[3]));
+        } else {
+            static_assert(N == 8, "elements per store");
+            *reinterpret_cast<uint4*>(o) = BF16::narrow(y);
+        }
+    }
+}
+
 // Floats as unsigned integers in the same order (no NaN; -0 counts as +0).
 __device__ inline uint32_t order_key(float f) {
     const uint32_t u = __float_as_uint(f + 0.0f);

@@ -49,7 +49,8 @@ struct AttnArgs {
     const float* scores_in;   // [num_seqs][heads][capacity] or null
     float* scores_out;
     int64_t capacity;
-    void* ws;                 // partial results
+    void* ws;                 // prefix sums of the sequences' steps, then the parts of the units
+    int64_t part_offset;      // bytes before the parts
     int32_t words;
     int32_t topk;
     int32_t heads;            // cache heads
@@ -109,8 +110,9 @@ struct EvictArgs {
 
 hipError_t launch_verify_tree(const StepArgs& a, const VerifyArgs& va, const TreeArgs& ta,
                               bool mx, int dtype, int D, int W, hipStream_t stream);
-hipError_t launch_tree_attention(const AttnArgs& a, bool mx, int dtype, int D, hipStream_t stream);
-hipError_t launch_block_attention(const AttnArgs& a, bool mx, int dtype, int D,
+hipError_t launch_tree_attention(const AttnArgs& a, bool mx, int dtype, int D, int row_tiles,
+                                 hipStream_t stream);
+hipError_t launch_block_attention(const AttnArgs& a, bool mx, int dtype, int D, int row_tiles,
                                   hipStream_t stream);
 hipError_t launch_cache_scores(const AttnArgs& a, bool mx, int dtype, int D, hipStream_t stream);
 hipError_t launch_block_summary(const SummaryArgs& a, bool mx, int dtype, int D,
