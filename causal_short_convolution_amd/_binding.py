@@ -88,7 +88,7 @@ def abi_version() -> int:
 
 
 def _ptr(t: Optional[torch.Tensor]):
-    return None if t is None else ctypes.c_void_p(t.data_ptr())
+    return None if t is None else t.data_ptr()  # an int: ctypes converts it by the argument type
 
 
 # ------------------------------------------------------------------------------------------------
@@ -125,9 +125,16 @@ class _Args:
         if t.dtype not in dtypes:
             want = " or ".join(str(d) for d in dtypes)
             self.fail(f"{name} must be {want}, got {t.dtype}")
-        if t.dim() != len(shape) or any(s is not None and s != n for s, n in zip(shape, t.shape)):
+        got = t.shape
+        fits = len(got) == len(shape)
+        if fits:
+            for s, n in zip(shape, got):
+                if s is not None and s != n:
+                    fits = False
+                    break
+        if not fits:
             want = "[" + ", ".join("*" if s is None else str(s) for s in shape) + "]"
-            self.fail(f"{name} must have shape {want}, got {list(t.shape)}")
+            self.fail(f"{name} must have shape {want}, got {list(got)}")
         if contiguous and not t.is_contiguous():
             self.fail(f"{name} must be contiguous")
         self._device(t, name)
@@ -199,7 +206,7 @@ def _flags(t):
 
 def _stream_handle(device, stream):
     s = stream if stream is not None else torch.cuda.current_stream(device)
-    return ctypes.c_void_p(s.cuda_stream)
+    return s.cuda_stream
 
 
 def _check(rc: int):

@@ -449,6 +449,24 @@ struct Tile<F32, MX, D> {
     }
 };
 
+// 32 mask bits of a row from bit `at` on; bits before 0 are the cached keys (ones).
+__device__ inline uint32_t mask_bits(const AttnArgs& a, int64_t t, int32_t i, int32_t at) {
+    if (at <= -32) return 0xffffffffu;
+    if (a.mask == nullptr) {
+        const int32_t n = i - at + 1;  // new tokens 0..i, and the cached keys before them
+        return n >= 32 ? 0xffffffffu : n <= 0 ? 0u : (1u << n) - 1u;
+    }
+    const uint64_t* m = reinterpret_cast<const uint64_t*>(a.mask) + t * a.words;
+    if (at < 0) {
+        const uint64_t w = a.words > 0 ? m[0] : 0;
+        return (uint32_t)(w << -at) | ((1u << -at) - 1u);
+    }
+    const int32_t j = at >> 6, sh = at & 63;
+    const uint64_t lo = j < a.words ? m[j] : 0;
+    const uint64_t hi = j + 1 < a.words ? m[j + 1] : 0;
+    return (uint32_t)(sh ? (lo >> sh) | (hi << (64 - sh)) : lo);
+}
+
 }  // namespace sc
 
 #endif  // SHORTCONV_ATTENTION_TILE_H
