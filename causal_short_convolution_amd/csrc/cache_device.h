@@ -163,6 +163,114 @@ __device__ inline void kth_largest(Key key, int n, int k, uint32_t* hist, uint32
     ties = rest;
 }
 
+// LDS of kth_of_registers.
+struct KthScratch {
+    static constexpr int kList = 1024;
+    uint32_t list[kList];
+    int counts[2][16];
+    uint32_t used, differ;
+};
+
+// Keys of the workgroup at or above `cand`, in every thread: a compare per key and a population
+// count of the wave's result, then one meeting of the waves. `turn` alternates the halves of
+// the counts, since the other half may still be read.
+template <int THREADS, int KPT>
+__device__ inline int count_at_least(const uint32_t (&key)[KPT], uint32_t cand, int turn,
+                                     KthScratch& sc) {
+    constexpr int WAVES = THREADS / 64;
+    int n = 0;
+#pragma unroll
+    for (int i = 0; i < KPT; ++i) n += __builtin_popcountll(__ballot(key[i] >= cand));
+    int* slot = sc.counts[turn & 1];
+    if ((threadIdx.x & 63) == 0) slot[threadIdx.x >> 6] = n;
+    __syncthreads();
+    n = 0;
+#pragma unroll
+    for (int w = 0; w < WAVES; ++w) n += slot[w];
+    return uniform(n);
+}
+
+// The k-th largest of n keys that a workgroup of THREADS threads holds in registers, key
+// i * THREADS + threadIdx.x in register i (0 past the n-th), 1 <= k <= n: bit by bit from the top, each bit kept if at least k keys reach the
+// value with it. Once few enough keys can still be it, those go to LDS and the remaining bits are
+// found among them, from the highest bit they differ in. Returns `threshold` and `ties`: the k
+// largest are the keys above the threshold and `ties` of those equal to it.
+template <int THREADS, int KPT>
+__device__ inline void kth_of_registers(const uint32_t (&key)[KPT], int n, int k, KthScratch& sc,
+                                        uint32_t& threshold, int& ties) {
+    constexpr int LPT = KthScratch::kList / THREADS;
+    uint32_t t = 0;
+    int above = 0;    // keys past those that can still be the k-th largest
+    int reach = n;    // keys at or above t
+    int bit = 31;
+    if (threadIdx.x == 0) sc.used = sc.differ = 0;
+    for (; bit >= 0 && reach - above > KthScratch::kList; --bit) {
+        const uint32_t cand = t | (1u << bit);
+        const int c = count_at_least<THREADS, KPT>(key, cand, bit, sc);
+        if (c >= k) {
+            t = cand;
+            reach = c;
+        } else {
+            above = c;
+        }
+        if (c == k) {  // exactly the keys from here on
+            threshold = cand - 1;
+            ties = 0;
+            return;
+        }
+    }
+    if (bit < 0) {
+        threshold = t;
+        ties = k - above;
+        return;
+    }
+    __syncthreads();  // `used` is cleared, and no wave still reads the counts
+    const uint32_t span = bit == 31 ? 0xffffffffu : (2u << bit) - 1u;  // keys t .. t + span are left
+#pragma unroll
+    for (int i = 0; i < KPT; ++i) {
+        // key >= t and key <= t + span, unsigned
+        const bool left = i * THREADS + (int)threadIdx.x < n && key[i] - t <= span;
+        const uint64_t m = __ballot(left);
+        if (m == 0) continue;
+        uint32_t at = 0;
+        if ((threadIdx.x & 63) == 0) at = atomicAdd(&sc.used, (uint32_t)__builtin_popcountll(m));
+        at = (uint32_t)uniform((int32_t)at) +
+             __builtin_amdgcn_mbcnt_hi((uint32_t)(m >> 32),
+                                       __builtin_amdgcn_mbcnt_lo((uint32_t)m, 0));
+        if (left && at < KthScratch::kList) sc.list[at] = key[i];
+    }
+    __syncthreads();
+    const int used = min((int)sc.used, KthScratch::kList);
+    const uint32_t probe = sc.list[0];
+    uint32_t mine[LPT], differ = 0;
+#pragma unroll
+    for (int i = 0; i < LPT; ++i) {
+        const int j = i * THREADS + threadIdx.x;
+        mine[i] = j < used ? sc.list[j] : 0u;
+        if (j < used) differ |= mine[i] ^ probe;
+    }
+    if (__ballot(differ != 0)) atomicOr(&sc.differ, differ);
+    __syncthreads();
+    differ = sc.differ;
+    // the bits that all share are the k-th largest's too
+    const int high = differ ? 31 - __builtin_clz(differ) : -1;
+    t = high == 31 ? 0u : high < 0 ? probe : probe & ~((2u << high) - 1u);
+    for (bit = high; bit >= 0; --bit) {
+        const uint32_t cand = t | (1u << bit);
+        const int c = above + count_at_least<THREADS, LPT>(mine, cand, bit, sc);
+        if (c >= k) t = cand;
+        if (c == k) {
+            threshold = cand - 1;
+            ties = 0;
+            return;
+        }
+    }
+    int more = 0;
+    if (t != 0xffffffffu) more = count_at_least<THREADS, LPT>(mine, t + 1, bit, sc);
+    threshold = t;
+    ties = k - above - more;
+}
+
 // Exclusive prefix sum over the workgroup of one small count per thread, and the total. `sums` is
 // LDS of one word per wave plus one.
 __device__ inline int block_prefix(int v, int* sums, int& total) {

@@ -17,26 +17,166 @@ __device__ inline int32_t entries_of(const EvictArgs& a, int s) {
     return n < 0 ? 0 : (int32_t)n;
 }
 
-__global__ void __launch_bounds__(kPlan) evict_plan_kernel(EvictArgs a) {
+// One head of one sequence.
+struct Head {
+    const float* scores;
+    const int32_t* positions;
+    float* scores_out;
+    int32_t* positions_out;
+    int32_t* dst;
+    int32_t* src;
+    int64_t index;
+    int64_t late;  // positions from here on are among the recent ones
+    int32_t sinks;
+    __device__ Head(const EvictArgs& a, int s, int h) {
+        index = (int64_t)s * a.heads + h;
+        scores = a.scores + index * a.capacity;
+        positions = a.positions + index * a.capacity;
+        scores_out = a.scores_out + index * a.capacity;
+        positions_out = a.positions_out + index * a.capacity;
+        dst = a.dst + index * a.max_moves;
+        src = a.src + index * a.max_moves;
+        late = (int64_t)a.seen[s] - a.recent;
+        sinks = a.sinks;
+    }
+    // Protected entries above all numbers, NaN below them.
+    __device__ uint32_t key(float f, int32_t pos) const {
+        if (pos < sinks || pos >= late) return 0xffffffffu;
+        return f != f ? 0u : order_key(f);
+    }
+    // Scores and positions of the kept entries: those that stay (unless the output is the input),
+    // then those that move, whose sources lie at or past the budget.
+    __device__ void write(int32_t kept, int32_t holes) const {
+        if (scores_out != scores || positions_out != positions) {
+            constexpr int U = 4;  // loads in flight
+            for (int j0 = threadIdx.x; j0 < kept; j0 += U * blockDim.x) {
+                float f[U];
+                int32_t p[U];
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+                    const int j = min(j0 + u * (int)blockDim.x, kept - 1);
+                    f[u] = scores[j];
+                    p[u] = positions[j];
+                }
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+                    const int j = j0 + u * (int)blockDim.x;
+                    if (j < kept) {
+                        scores_out[j] = f[u];
+                        positions_out[j] = p[u];
+                    }
+                }
+            }
+        }
+        __syncthreads();
+        for (int j = threadIdx.x; j < holes; j += blockDim.x) {
+            const int32_t from = src[j], to = dst[j];
+            scores_out[to] = scores[from];
+            positions_out[to] = positions[from];
+        }
+    }
+};
+
+// Up to KPT entries per thread, entry i * THREADS + tid in register i, ranked there. The order of the
+// entries is (i, wave, lane): places within a list come from a wave's ballots and a scan over the
+// counts of all (i, wave).
+template <int THREADS, int KPT>
+__global__ void __launch_bounds__(THREADS) evict_plan_kernel(EvictArgs a) {
+    constexpr int WAVES = THREADS / 64;
+    __shared__ KthScratch scratch;
+    __shared__ int sums[WAVES + 1];
+    __shared__ int first[2][KPT * WAVES];
+    const int h = blockIdx.x, s = blockIdx.y, tid = threadIdx.x;
+    const int wave = uniform(tid >> 6);
+    const int32_t n = entries_of(a, s);
+    const Head head(a, s, h);
+    const int32_t kept = min(n, a.budget);
+    int holes = 0;
+    if (n > a.budget && kept > 0) {
+        uint32_t key[KPT];
+        {
+            float f[KPT];
+            int32_t p[KPT];
+#pragma unroll
+            for (int i = 0; i < KPT; ++i) {
+                const int j = min(i * THREADS + tid, n - 1);
+                f[i] = head.scores[j];
+                p[i] = head.positions[j];
+            }
+#pragma unroll
+            for (int i = 0; i < KPT; ++i) key[i] = i * THREADS + tid < n ? head.key(f[i], p[i]) : 0u;
+        }
+        uint32_t threshold;
+        int ties, total;
+        kth_of_registers<THREADS, KPT>(key, n, kept, scratch, threshold, ties);
+        auto below = [](uint64_t mask) {  // bits of lower lanes
+            return (int)__builtin_amdgcn_mbcnt_hi((uint32_t)(mask >> 32),
+                                                  __builtin_amdgcn_mbcnt_lo((uint32_t)mask, 0));
+        };
+        auto scan = [&](int list) {
+            __syncthreads();
+            static_assert(KPT * WAVES <= THREADS, "one count per thread");
+            const int c = tid < KPT * WAVES ? first[list][tid] : 0;
+            const int x = block_prefix(c, sums, total);
+            if (tid < KPT * WAVES) first[list][tid] = x;
+            __syncthreads();
+            return total;
+        };
+        if (ties > 0) {  // the lowest of the equal entries
+#pragma unroll
+            for (int i = 0; i < KPT; ++i) {
+                const uint64_t m = __ballot(key[i] == threshold && i * THREADS + tid < n);
+                if ((tid & 63) == 0) first[0][i * WAVES + wave] = __builtin_popcountll(m);
+            }
+            scan(0);
+        }
+#pragma unroll
+        for (int i = 0; i < KPT; ++i) {  // from here on key[i] is 1 for an entry to keep
+            bool keep = key[i] > threshold;
+            if (ties > 0) {
+                const bool tie = key[i] == threshold && i * THREADS + tid < n;
+                keep |= tie && first[0][i * WAVES + wave] + below(__ballot(tie)) < ties;
+            }
+            key[i] = keep;
+        }
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < KPT; ++i) {
+            const int j = i * THREADS + tid;
+            const uint64_t hole = __ballot(!key[i] && j < kept);
+            const uint64_t move = __ballot(key[i] && j >= kept);
+            if ((tid & 63) == 0) {
+                first[0][i * WAVES + wave] = __builtin_popcountll(hole);
+                first[1][i * WAVES + wave] = __builtin_popcountll(move);
+            }
+        }
+        holes = scan(0);
+        scan(1);
+#pragma unroll
+        for (int i = 0; i < KPT; ++i) {
+            const int j = i * THREADS + tid;
+            const bool hole = !key[i] && j < kept;
+            const bool move = key[i] && j >= kept;
+            const uint64_t mh = __ballot(hole), mm = __ballot(move);
+            if (hole) head.dst[first[0][i * WAVES + wave] + below(mh)] = j;
+            if (move) head.src[first[1][i * WAVES + wave] + below(mm)] = j;
+        }
+        __syncthreads();
+    }
+    if (tid == 0) a.count[head.index] = holes;
+    head.write(kept, holes);
+}
+
+// More entries than registers hold: the keys are read again for every 8 bits of the threshold and
+// once more, in order, to split them.
+__global__ void __launch_bounds__(kPlan) evict_plan_long_kernel(EvictArgs a) {
     __shared__ uint32_t hist[258];
     __shared__ int sums[kPlan / 64 + 1];
     const int h = blockIdx.x, s = blockIdx.y, tid = threadIdx.x;
     const int32_t n = entries_of(a, s);
-    const int64_t head = (int64_t)s * a.heads + h;
-    const float* scores = a.scores + head * a.capacity;
-    const int32_t* positions = a.positions + head * a.capacity;
-    float* scores_out = a.scores_out + head * a.capacity;
-    int32_t* positions_out = a.positions_out + head * a.capacity;
+    const Head head(a, s, h);
     const int32_t kept = min(n, a.budget);
-    int32_t* dst = a.dst + head * a.max_moves;
-    int32_t* src = a.src + head * a.max_moves;
-    const int64_t late = (int64_t)a.seen[s] - a.recent;
-    auto key = [&](int j) {
-        const int32_t pos = positions[j];
-        if (pos < a.sinks || pos >= late) return 0xffffffffu;
-        const float f = scores[j];
-        return f != f ? 0u : order_key(f);
-    };
+    auto key = [&](int j) { return head.key(head.scores[j], head.positions[j]); };
     int holes = 0, movers = 0;
     if (n > a.budget && kept > 0) {
         uint32_t threshold;
@@ -54,28 +194,16 @@ __global__ void __launch_bounds__(kPlan) evict_plan_kernel(EvictArgs a) {
             const bool move = j >= kept && keep;
             const int hi = holes + block_prefix(hole, sums, n_hole);
             const int mi = movers + block_prefix(move, sums, n_move);
-            if (hole) dst[hi] = j;
-            if (move) src[mi] = j;
+            if (hole) head.dst[hi] = j;
+            if (move) head.src[mi] = j;
             tied += n_tie;
             holes += n_hole;
             movers += n_move;
         }
         __syncthreads();
     }
-    if (tid == 0) a.count[head] = holes;
-    // the entries that stay, then the ones that move (their sources lie at or past the budget)
-    for (int j = tid; j < kept; j += kPlan) {
-        const float f = scores[j];
-        const int32_t p = positions[j];
-        scores_out[j] = f;
-        positions_out[j] = p;
-    }
-    __syncthreads();
-    for (int j = tid; j < holes; j += kPlan) {
-        const int32_t from = src[j], to = dst[j];
-        scores_out[to] = scores[from];
-        positions_out[to] = positions[from];
-    }
+    if (tid == 0) a.count[head.index] = holes;
+    head.write(kept, holes);
 }
 
 // Copies the moved rows: BYTES = one head's row in one tensor, in 16-byte pieces, plus its scale
@@ -121,7 +249,16 @@ void move(const EvictArgs& a, hipStream_t st) {
 }  // namespace
 
 hipError_t launch_cache_evict(const EvictArgs& a, bool mx, int dtype, int D, hipStream_t st) {
-    evict_plan_kernel<<<dim3((uint32_t)a.heads, (uint32_t)a.num_seqs), kPlan, 0, st>>>(a);
+    const dim3 grid((uint32_t)a.heads, (uint32_t)a.num_seqs);
+    const int64_t cap = (int64_t)a.pg.max_blocks << a.pg.shift;
+    const int64_t most = a.capacity < cap ? a.capacity : cap;  // entries of a head
+    // Few threads per head while their registers hold it: a bit costs every wave the meeting.
+    if (most <= 8 * 256) evict_plan_kernel<256, 8><<<grid, 256, 0, st>>>(a);
+    else if (most <= 20 * 256) evict_plan_kernel<256, 20><<<grid, 256, 0, st>>>(a);
+    else if (most <= 16 * 1024) evict_plan_kernel<1024, 16><<<grid, 1024, 0, st>>>(a);
+    else if (most <= 32 * 1024) evict_plan_kernel<1024, 32><<<grid, 1024, 0, st>>>(a);
+    else if (most <= 64 * 1024) evict_plan_kernel<1024, 64><<<grid, 1024, 0, st>>>(a);
+    else evict_plan_long_kernel<<<grid, kPlan, 0, st>>>(a);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
     if (mx) {

@@ -205,13 +205,19 @@ def test_capacity_below_the_lengths():
 
 
 @pytest.mark.parametrize("lens,budget", [((2500, 1030), 1024), ((5000,), 4999), ((9000, 8191), 3),
-                                         ((20000,), 9000)])
+                                         ((20000,), 9000), ((40000, 9), 3000)])
 def test_long_rows(lens, budget):
     """More entries than a workgroup has threads; distinct scores."""
     c = Cut(8, lens=lens, budget=budget, H=2, recent=64, special=False, shuffled=False)
     g = np.random.default_rng(8)
     c.scores[:] = np.exp(2 * g.standard_normal(c.scores.shape)).astype(np.float32)
     c.scores[g.random(c.scores.shape) < 0.2] = 0.0
+    c.check()
+
+
+def test_more_entries_than_registers_hold():
+    c = Cut(11, lens=(70000, 300), budget=900, H=1, recent=64, special=False, shuffled=False)
+    c.scores[:] = np.random.default_rng(11).integers(0, 3000, c.scores.shape).astype(np.float32)
     c.check()
 
 
