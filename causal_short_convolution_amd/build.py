@@ -19,9 +19,9 @@ LIB = os.path.join(HERE, "libshortconv.so")
 SOURCES = [os.path.join(CSRC, f) for f in ("kernels.hip", "backward.hip", "abi.hip")]
 # the operators on the paged cache, a library of its own (include/shortconv_cache.h)
 CACHE_LIB = os.path.join(HERE, "libshortconv_cache.so")
-CACHE_SOURCES = [os.path.join(CSRC, f) for f in ("tree_verify.hip", "cache_attention.hip",
-                                                 "cache_blocks.hip", "cache_evict.hip", "cache_scores.hip",
-                                                 "cache_abi.hip")]
+CACHE_SOURCES = [os.path.join(CSRC, f) for f in (
+    "tree_verify.hip", "cache_attention.hip", "wide_attention.hip", "cache_blocks.hip",
+    "cache_scores.hip", "cache_evict.hip", "cache_abi.hip")]
 # measurement companion used by bench.py (same-bytes copy ceiling); not part of the C ABI
 PROBE_LIB = os.path.join(HERE, "libscprobe.so")
 PROBE_SOURCES = [os.path.join(CSRC, "copy_probe.hip")]

@@ -1,0 +1,239 @@
+// The line of steps that the attention kernels share out: units of work, their place in the line,
+// each worker's run, and the launch that joins the parts of units which crossed workers.
+#ifndef SHORTCONV_ATTENTION_LINE_H
+#define SHORTCONV_ATTENTION_LINE_H
+
+#include "attention_tile.h"
+#include "cache_attention.h"
+
+namespace sc {
+
+// `total` steps over WORKERS workers: worker w owns [begin(w), begin(w + 1)).
+template <int WORKERS>
+struct Shares {
+    int64_t total, each, more;
+    int32_t workers;
+    __device__ Shares(int64_t t) : total(t) {
+        workers = (int32_t)(t < WORKERS ? t : WORKERS);
+        each = workers ? t / workers : 0;
+        more = workers ? t - each * workers : 0;
+    }
+    __device__ int64_t begin(int32_t w) const { return w * each + (w < more ? w : more); }
+    __device__ int32_t owner(int64_t step) const {
+        const int64_t cut = more * (each + 1);
+        return (int32_t)(step < cut ? step / (each + 1) : more + (step - cut) / each);
+    }
+    // The worker that this workgroup is. Workgroups go round the 8 XCDs by blockIdx. Where every
+    // worker has steps, consecutive runs go to one XCD, so that units that read the same rows
+    // meet in its L2; fewer steps than workers are spread over the XCDs.
+    __device__ int32_t me() const {
+        return total < WORKERS ? (int32_t)blockIdx.x
+                               : (int32_t)(blockIdx.x & 7) * (WORKERS / 8) +
+                                     (int32_t)(blockIdx.x >> 3);
+    }
+};
+
+// One unit of work: a cache head of a sequence (of a token, for selected pages) and up to M of the
+// query rows that read it.
+struct Unit {
+    int32_t s;          // sequence
+    int32_t h;          // cache head
+    int32_t row0;       // first query row (of the sequence's len * group, or the token's group)
+    int32_t rows;       // rows in this unit, 1 .. M
+    int32_t steps;      // steps of all its keys, at least 1
+    int64_t tok;        // selected pages: the token
+    int64_t first;      // its first step in the line
+};
+
+// Sizes in steps of KS keys and units of M rows.
+template <int KS, int M>
+struct Steps {
+    __device__ static inline int64_t of_keys(int64_t keys) {
+        return keys > KS ? (keys + KS - 1) / KS : 1;
+    }
+    // Steps of a sequence: its cache heads, times its row tiles, times its key steps.
+    __device__ static inline int64_t of_sequence(const AttnArgs& a, const SeqInfo& q) {
+        if (q.len == 0) return 0;
+        const int64_t tiles = ((int64_t)q.len * a.group + M - 1) / M;
+        return a.heads * tiles * of_keys(q.keys);
+    }
+    __device__ static inline int32_t of_pages(const AttnArgs& a) {
+        return (int32_t)of_keys((int64_t)a.topk << a.pg.shift);
+    }
+    __device__ static inline int32_t group_tiles(const AttnArgs& a) {
+        return (a.group + M - 1) / M;
+    }
+};
+
+// LDS of find_run.
+struct RunScratch {
+    int64_t sums[16];
+    int64_t first;
+    int32_t s;
+};
+
+// By the whole workgroup: the number of steps of all sequences; in `scratch` the sequence that this
+// worker's first step lies in and that sequence's first step. The first worker leaves the prefix
+// sums for the joining launch in `prefix`.
+template <int KS, int M, int WORKERS, int THREADS>
+__device__ inline int64_t find_run(const AttnArgs& a, int64_t* prefix, RunScratch& scratch) {
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    const int per = (a.b.num_seqs + THREADS - 1) / THREADS;
+    int64_t mine = 0;
+    for (int j = 0; j < per; ++j) {
+        const int s = tid * per + j;
+        if (s < a.b.num_seqs) mine += Steps<KS, M>::of_sequence(a, seq_info(a.b, a.pg, s));
+    }
+    int64_t inc = mine;
+    for (int d = 1; d < 64; d <<= 1) {
+        const int64_t o = __shfl_up(inc, d);
+        if (lane >= d) inc += o;
+    }
+    if (lane == 63) scratch.sums[wave] = inc;
+    __syncthreads();
+    int64_t before = 0, total = 0;
+    for (int w = 0; w < THREADS / 64; ++w) {
+        if (w < wave) before += scratch.sums[w];
+        total += scratch.sums[w];
+    }
+    const Shares<WORKERS> sh(total);
+    const int32_t me = sh.me();
+    const int64_t want = me < sh.workers ? sh.begin(me) : -1;
+    int64_t x = before + inc - mine;
+    for (int j = 0; j < per; ++j) {
+        const int s = tid * per + j;
+        if (s >= a.b.num_seqs) break;
+        const int64_t n = Steps<KS, M>::of_sequence(a, seq_info(a.b, a.pg, s));
+        if (want >= x && want < x + n) {
+            scratch.s = s;
+            scratch.first = x;
+        }
+        if (me == 0) prefix[s] = x;
+        x += n;
+    }
+    if (me == 0 && tid == THREADS - 1) prefix[a.b.num_seqs] = total;
+    __syncthreads();
+    return total;
+}
+
+// The unit of step `at` in a line of whole sequences; u.s, q and seq_first (the first step of
+// sequence u.s) move on as needed.
+template <int KS, int M>
+__device__ inline void unit_of_step(const AttnArgs& a, int64_t at, Unit& u, SeqInfo& q,
+                                    int64_t& seq_first) {
+    int64_t n = Steps<KS, M>::of_sequence(a, q);
+    while (at >= seq_first + n) {
+        seq_first += n;
+        q = seq_info(a.b, a.pg, ++u.s);
+        n = Steps<KS, M>::of_sequence(a, q);
+    }
+    u.steps = (int32_t)Steps<KS, M>::of_keys(q.keys);
+    const int64_t rows = (int64_t)q.len * a.group;
+    const int64_t tiles = (rows + M - 1) / M;
+    const int64_t index = (at - seq_first) / u.steps;
+    u.first = seq_first + index * u.steps;
+    u.h = (int32_t)(index / tiles);
+    const int64_t r0 = index % tiles * M;
+    u.row0 = (int32_t)r0;
+    u.rows = (int32_t)(rows - r0 < M ? rows - r0 : M);
+    u.tok = q.start;
+}
+
+// A part of a unit that worker `me` computed, in the workspace: M rows of D sums, then the rows'
+// maxima and sums of weights. Slot 1 if it holds the unit's first step (the worker's last part),
+// else slot 0 (its first).
+template <int M, int D>
+__device__ inline float* part_of(void* ws, int64_t offset, int32_t worker, bool holds_first) {
+    return reinterpret_cast<float*>(static_cast<char*>(ws) + offset) +
+           ((int64_t)worker * 2 + holds_first) * (M * (D + 2));
+}
+
+// Adds to y (channels d.. of one row of token t) the infinities and NaN that V has in the new tokens
+// of key positions [k0, k1) that the row looks at, and that the products left out.
+template <class E, bool MX, int D, int N>
+__device__ inline void add_left_out(const AttnArgs& a, const SeqInfo& q, const Unit& u, int64_t t,
+                                    int64_t k0, int64_t k1, int d, float (&y)[N]) {
+    const int32_t last = (int32_t)min((int64_t)q.keys, k1);
+    for (int32_t k = (int32_t)max((int64_t)q.ctx, k0); k < last; ++k) {
+        if (!(mask_bits(a, t, (int32_t)(t - q.start), k - q.ctx) & 1)) continue;
+        const int32_t slot = slot_of(a.pg, u.s, k);
+        if (slot < 0) continue;
+        const int64_t e0 = ((int64_t)slot * a.heads + u.h) * D + d;
+#pragma unroll
+        for (int e = 0; e < N; ++e) {
+            const float f = cache_element<E, MX>(a.cache[1], a.scales[1], e0 + e);
+            if ((__float_as_uint(f) & 0x7f800000u) == 0x7f800000u) y[e] += f;
+        }
+    }
+}
+
+// Joins the parts of the units that crossed workers: one wave per (token, query head).
+template <class E, int D, int KS, int M, int WORKERS, bool SPARSE>
+__global__ void __launch_bounds__(256) join_kernel(AttnArgs a) {
+    using S = Steps<KS, M>;
+    constexpr int N = D / 64;
+    const int lane = threadIdx.x & 63;
+    const int64_t t = blockIdx.x;
+    const int hq = uniform((int)(blockIdx.y * 4 + (threadIdx.x >> 6)));
+    if (hq >= a.heads * a.group) return;
+    const int s = seq_of_token(a.b, t);
+    const SeqInfo q = seq_info(a.b, a.pg, s);
+    const int64_t i = t - q.start;
+    if (i < 0 || i >= q.len) return;
+    const char* ws = static_cast<const char*>(a.ws);
+    const int h = hq / a.group;
+    int64_t first, total;
+    int32_t steps, row;
+    if constexpr (SPARSE) {
+        steps = S::of_pages(a);
+        const int32_t tiles = S::group_tiles(a);
+        row = hq - h * a.group;
+        first = ((t * a.heads + h) * tiles + row / M) * steps;
+        total = a.b.tokens * a.heads * tiles * steps;
+    } else {
+        const int64_t* prefix = reinterpret_cast<const int64_t*>(ws);
+        steps = (int32_t)S::of_keys(q.keys);
+        const int64_t tiles = ((int64_t)q.len * a.group + M - 1) / M;
+        row = (int32_t)(i * a.group + hq - h * a.group);
+        first = prefix[s] + (h * tiles + row / M) * steps;
+        total = prefix[a.b.num_seqs];
+    }
+    row %= M;
+    const Shares<WORKERS> sh(total);
+    const int32_t w0 = sh.owner(first), w1 = sh.owner(first + steps - 1);
+    if (w0 == w1) return;  // written by its worker
+    auto part = [&](int32_t w) { return part_of<M, D>(a.ws, a.part_offset, w, w == w0); };
+    float big = -__builtin_inff();
+    for (int32_t w = w0; w <= w1; ++w) big = __builtin_fmaxf(big, part(w)[M * D + row]);
+    const float base = big == -__builtin_inff() ? 0.0f : big;
+    float sum = 0.0f, o[N];
+#pragma unroll
+    for (int j = 0; j < N; ++j) o[j] = 0.0f;
+    for (int32_t w = w0; w <= w1; ++w) {
+        const float* p = part(w);
+        const float f = exp2_fast(p[M * D + row] - base);
+        sum += p[M * D + M + row] * f;
+#pragma unroll
+        for (int j = 0; j < N; ++j)
+            o[j] = __builtin_fmaf(p[row * D + lane * N + j], f, o[j]);
+    }
+    const bool some = sum > 0.0f || sum != sum;
+    const float inv = some ? 1.0f / sum : 0.0f;
+#pragma unroll
+    for (int j = 0; j < N; ++j) o[j] *= inv;
+    const int64_t at = t * a.heads * a.group + hq;
+    store_row<E, N>(a.out, at * D + lane * N, o);
+    if (a.lse != nullptr && lane == 0)
+        a.lse[at] = some ? (big + log2_fast(sum)) * kLn2 : -__builtin_inff();
+}
+
+template <class E, int D, int KS, int M, int WORKERS, bool SPARSE>
+hipError_t launch_join(const AttnArgs& a, hipStream_t st) {
+    const dim3 grid((uint32_t)a.b.tokens, (uint32_t)(a.heads * a.group + 3) / 4);
+    join_kernel<E, D, KS, M, WORKERS, SPARSE><<<grid, 256, 0, st>>>(a);
+    return hipGetLastError();
+}
+
+}  // namespace sc
+
+#endif  // SHORTCONV_ATTENTION_LINE_H

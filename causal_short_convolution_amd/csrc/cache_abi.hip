@@ -3,7 +3,6 @@
 #include <stdarg.h>
 #include <stdio.h>
 
-#include "cache_attention.h"
 #include "cache_internal.h"
 #include "shortconv_cache.h"
 
@@ -201,11 +200,12 @@ int verify_tree(const char* fn, bool mx, const void* k, const void* v, int64_t k
 // ------------------------------------------------------------------------------------------------
 enum Kind { TREE, BLOCKS, SCORES };
 
-// Query rows that share a unit: those of an average sequence, or of one token.
-int unit_row_tiles(Kind kind, int64_t tokens, int32_t num_seqs, int32_t q_heads, int32_t heads) {
+// The units' shape, from the query rows of an average sequence, or of one token.
+sc::AttnShape unit_shape(Kind kind, int64_t tokens, int32_t num_seqs, int32_t q_heads,
+                         int32_t heads, int32_t D, int32_t dtype) {
     const int64_t group = q_heads / heads;
     const int64_t each = kind == TREE && num_seqs > 0 ? (tokens + num_seqs - 1) / num_seqs : 1;
-    return sc::row_tiles(each * group);
+    return sc::attention_shape(kind == TREE, each * group, element_bytes(dtype), D);
 }
 
 int64_t part_offset(int32_t num_seqs) { return ((int64_t)num_seqs + 1) * 8 / 256 * 256 + 256; }
@@ -213,10 +213,10 @@ int64_t part_offset(int32_t num_seqs) { return ((int64_t)num_seqs + 1) * 8 / 256
 // The prefix sums of the sequences' steps (tree), and two parts per worker: rows of D sums, then
 // the rows' maxima and sums.
 size_t attention_workspace(Kind kind, int64_t tokens, int32_t num_seqs, int32_t q_heads,
-                           int32_t heads, int32_t D) {
-    const int R = unit_row_tiles(kind, tokens, num_seqs, q_heads, heads);
+                           int32_t heads, int32_t D, int32_t dtype) {
+    const sc::AttnShape shape = unit_shape(kind, tokens, num_seqs, q_heads, heads, D, dtype);
     return part_offset(kind == TREE ? num_seqs : 0) +
-           (size_t)sc::workers(D) * 2 * 16 * R * (D + 2) * sizeof(float);
+           (size_t)shape.worker_count(D) * 2 * shape.rows() * (D + 2) * sizeof(float);
 }
 
 int attention(const char* fn, Kind kind, bool mx, const void* q, int64_t q_stride,
@@ -255,7 +255,7 @@ int attention(const char* fn, Kind kind, bool mx, const void* q, int64_t q_strid
     SC_TRY(check_aligned(fn, ptrs, 5));
     const size_t need = kind == SCORES ? 0
                                        : attention_workspace(kind, tokens, num_seqs, q_heads,
-                                                             heads, D);
+                                                             heads, D, dtype);
     if (need > 0 && (!ws || ws_bytes < need))
         return fail(SC_ERR_INVALID, "%s: workspace of %zu bytes needed, %zu given", fn, need,
                     ws ? ws_bytes : (size_t)0);
@@ -284,9 +284,10 @@ int attention(const char* fn, Kind kind, bool mx, const void* q, int64_t q_strid
     a.scale = scale;
     const hipStream_t st = (hipStream_t)stream;
     if (kind == SCORES) return launched(fn, sc::launch_cache_scores(a, mx, dtype, D, st));
-    const int R = unit_row_tiles(kind, tokens, num_seqs, q_heads, heads);
-    return launched(fn, kind == TREE ? sc::launch_tree_attention(a, mx, dtype, D, R, st)
-                                     : sc::launch_block_attention(a, mx, dtype, D, R, st));
+    const sc::AttnShape shape = unit_shape(kind, tokens, num_seqs, q_heads, heads, D, dtype);
+    return launched(fn, shape.waves ? sc::launch_wide_attention(a, mx, D, shape, st)
+                                    : sc::launch_attention(a, kind == BLOCKS, mx, dtype, D,
+                                                           shape.tiles, st));
 }
 
 size_t bad_size(const char* fn, const char* why) {
@@ -456,7 +457,8 @@ SC_API size_t shortconv_tree_attention_workspace_size(int64_t total_tokens, int3
         return SIZE_MAX;
     if (total_tokens < 0 || total_tokens > INT32_MAX || num_seqs < 0)
         return bad_size(fn, "bad total_tokens or num_seqs");
-    return attention_workspace(TREE, total_tokens, num_seqs, num_q_heads, num_heads, head_dim);
+    return attention_workspace(TREE, total_tokens, num_seqs, num_q_heads, num_heads, head_dim,
+                               dtype);
 }
 
 SC_API int shortconv_block_summary(const void* k_cache, const int32_t* cu_seqlens,
@@ -581,7 +583,7 @@ SC_API size_t shortconv_block_attention_workspace_size(int64_t total_tokens, int
         return SIZE_MAX;
     if (total_tokens < 0 || total_tokens > INT32_MAX || topk < 0 || block_size < 1)
         return bad_size(fn, "bad total_tokens, topk or block_size");
-    return attention_workspace(BLOCKS, total_tokens, 0, num_q_heads, num_heads, head_dim);
+    return attention_workspace(BLOCKS, total_tokens, 0, num_q_heads, num_heads, head_dim, dtype);
 }
 
 SC_API int shortconv_cache_scores(const void* q, int64_t q_tok_stride, const float* lse,

@@ -11,8 +11,7 @@
 // of the unit they meet in LDS. A unit that ends inside one workgroup's run is written at once;
 // one that crosses workgroups leaves its unnormalized sums in the workspace, and a second launch
 // joins them (a fixed order: the same inputs give the same bits).
-#include "attention_tile.h"
-#include "cache_attention.h"
+#include "attention_line.h"
 
 namespace sc {
 namespace {
@@ -20,65 +19,14 @@ namespace {
 constexpr int kBlock = 256;
 constexpr int kWaves = 4;
 
-// Step w of `total` steps over `workers` workers: worker i owns [share_begin(i), share_begin(i+1)).
-template <int WORKERS>
-struct Shares {
-    int64_t total, each, more;
-    int32_t workers;
-    __device__ Shares(int64_t t) : total(t) {
-        workers = (int32_t)(t < WORKERS ? t : WORKERS);
-        each = workers ? t / workers : 0;
-        more = workers ? t - each * workers : 0;
-    }
-    __device__ int64_t begin(int32_t w) const { return w * each + (w < more ? w : more); }
-    __device__ int32_t owner(int64_t step) const {
-        const int64_t cut = more * (each + 1);
-        return (int32_t)(step < cut ? step / (each + 1) : more + (step - cut) / each);
-    }
-};
-
-// One unit of work and its query rows.
-struct Unit {
-    int32_t s;          // sequence
-    int32_t h;          // cache head
-    int32_t row0;       // first query row (of the sequence's len * group, or the token's group)
-    int32_t rows;       // rows in this unit, 1 .. 16 R
-    int32_t steps;      // steps of all its keys, at least 1
-    int64_t tok;        // selected pages: the token
-    int64_t first;      // its first step in the line
-};
-
-template <class E, bool MX, int D, int R, bool SPARSE>
-struct Geometry {
-    using T = Tile<E, MX, D>;
-    static constexpr int M = 16 * R;
-    static constexpr int KW = 16 * T::SUB;        // keys per wave and step
-    static constexpr int KS = KW * kWaves;        // keys per step
-    __device__ static inline int64_t key_steps(int64_t keys) {
-        return keys > KS ? (keys + KS - 1) / KS : 1;
-    }
-    // Steps of a sequence: its cache heads, times its row tiles, times its key steps.
-    __device__ static inline int64_t seq_steps(const AttnArgs& a, const SeqInfo& q) {
-        if (q.len == 0) return 0;
-        const int64_t tiles = ((int64_t)q.len * a.group + M - 1) / M;
-        return a.heads * tiles * key_steps(q.keys);
-    }
-    __device__ static inline int32_t block_steps(const AttnArgs& a) {
-        return (int32_t)key_steps((int64_t)a.topk << a.pg.shift);
-    }
-    __device__ static inline int32_t group_tiles(const AttnArgs& a) {
-        return (a.group + M - 1) / M;
-    }
-};
-
 template <class E, bool MX, int D, int R, bool SPARSE, bool PAGE16>
 __global__ void __launch_bounds__(kBlock, workers_per_cu(D)) attention_kernel(AttnArgs a) {
-    using G = Geometry<E, MX, D, R, SPARSE>;
     using T = Tile<E, MX, D>;
-    constexpr int kWorkers = workers(D);
-    constexpr int M = G::M;
-    constexpr int KW = G::KW;
+    constexpr int WORKERS = workers(D);
+    constexpr int M = 16 * R;
     constexpr int SUB = T::SUB;
+    constexpr int KW = 16 * SUB;      // keys per wave and step
+    constexpr int KS = KW * kWaves;   // keys per step
     constexpr uint32_t kFull = SUB == 2 ? 0xffffffffu : 0xffffu;
     constexpr int QSTRIDE = D * T::QB + 16;  // query rows in LDS, staggered over the banks
     constexpr bool QREG = R == 1 && D <= 128;  // query operands stay in registers
@@ -86,22 +34,12 @@ __global__ void __launch_bounds__(kBlock, workers_per_cu(D)) attention_kernel(At
     constexpr int kLds = 2 * M * OSTRIDE * 4 > M * QSTRIDE ? 2 * M * OSTRIDE * 4 : M * QSTRIDE;
     __shared__ __attribute__((aligned(16))) char lds[kLds];
     __shared__ float stat[kWaves][2][M];
-    __shared__ int64_t sums[kWaves];
-    __shared__ int32_t found_s;
-    __shared__ int64_t found_first;
+    __shared__ RunScratch run;
     __shared__ int32_t left_out_any;
 
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = uniform(tid >> 6);
     const int c = lane & 15, g = lane >> 4;
-    // Workgroups go round the 8 XCDs by blockIdx. Where every worker has steps, consecutive runs
-    // go to one XCD, so that units that read the same rows meet in its L2; fewer steps than
-    // workers are spread over the XCDs.
-    auto worker = [&](int64_t steps) {
-        return steps < kWorkers ? (int32_t)blockIdx.x
-                                : (int32_t)(blockIdx.x & 7) * (kWorkers / 8) +
-                                      (int32_t)(blockIdx.x >> 3);
-    };
     const int eb = MX ? 1 : E::BYTES;
     const uint32_t row_bytes = (uint32_t)(a.heads * D * eb);
     char* ws = static_cast<char*>(a.ws);
@@ -110,68 +48,30 @@ __global__ void __launch_bounds__(kBlock, workers_per_cu(D)) attention_kernel(At
     int64_t total, at, end;
     Unit u;
     if constexpr (SPARSE) {
-        u.steps = G::block_steps(a);
-        total = a.b.tokens * a.heads * G::group_tiles(a) * u.steps;
+        u.steps = Steps<KS, M>::of_pages(a);
+        total = a.b.tokens * a.heads * Steps<KS, M>::group_tiles(a) * u.steps;
     } else {
-        const int per = (a.b.num_seqs + kBlock - 1) / kBlock;
-        int64_t mine = 0;
-        for (int j = 0; j < per; ++j) {
-            const int s = tid * per + j;
-            if (s < a.b.num_seqs) mine += G::seq_steps(a, seq_info(a.b, a.pg, s));
-        }
-        int64_t inc = mine;
-        for (int d = 1; d < 64; d <<= 1) {
-            const int64_t o = __shfl_up(inc, d);
-            if (lane >= d) inc += o;
-        }
-        if (lane == 63) sums[wave] = inc;
-        __syncthreads();
-        int64_t before = 0;
-        total = 0;
-        for (int w = 0; w < kWaves; ++w) {
-            if (w < wave) before += sums[w];
-            total += sums[w];
-        }
-        const Shares<kWorkers> sh(total);
-        const int32_t me = worker(total);
-        const int64_t want = me < sh.workers ? sh.begin(me) : -1;
-        int64_t x = before + inc - mine;
-        int64_t* prefix = reinterpret_cast<int64_t*>(ws);
-        for (int j = 0; j < per; ++j) {
-            const int s = tid * per + j;
-            if (s >= a.b.num_seqs) break;
-            const int64_t n = G::seq_steps(a, seq_info(a.b, a.pg, s));
-            if (want >= x && want < x + n) {
-                found_s = s;
-                found_first = x;
-            }
-            if (me == 0) prefix[s] = x;
-            x += n;
-        }
-        if (me == 0 && tid == kBlock - 1) prefix[a.b.num_seqs] = total;
-        __syncthreads();
+        total = find_run<KS, M, WORKERS, kBlock>(a, reinterpret_cast<int64_t*>(ws), run);
     }
-    const Shares<kWorkers> sh(total);
-    const int32_t me = worker(total);
+    const Shares<WORKERS> sh(total);
+    const int32_t me = sh.me();
     if (me >= sh.workers) return;
     at = sh.begin(me);
     end = sh.begin(me + 1);
     SeqInfo q;
-    int32_t tiles;
     int64_t seq_first = 0;
     if constexpr (!SPARSE) {
-        u.s = uniform(found_s);
-        seq_first = uniform(found_first);
+        u.s = uniform(run.s);
+        seq_first = uniform(run.first);
         q = seq_info(a.b, a.pg, u.s);
     }
 
     while (at < end) {
         // ---- the unit that step `at` belongs to
-        int64_t tok = 0;   // first token of its rows
         int32_t last = 0;  // selected pages: the token's own position
         bool real = true;
         if constexpr (SPARSE) {
-            tiles = G::group_tiles(a);
+            const int32_t tiles = Steps<KS, M>::group_tiles(a);
             const int64_t n = at / u.steps;
             u.first = n * u.steps;
             const int32_t tile = (int32_t)(n % tiles);
@@ -180,29 +80,15 @@ __global__ void __launch_bounds__(kBlock, workers_per_cu(D)) attention_kernel(At
             u.tok = th / a.heads;
             u.s = seq_of_token(a.b, u.tok);
             q = seq_info(a.b, a.pg, u.s);
-            tok = u.tok;
-            const int64_t i = tok - q.start;
+            const int64_t i = u.tok - q.start;
             real = i >= 0 && i < q.len;  // a token behind the last sequence has no output
             last = (int32_t)min((int64_t)(a.pg.max_blocks << a.pg.shift) - 1, (int64_t)q.ctx + i);
             u.row0 = tile * M;
             u.rows = min(M, a.group - u.row0);
         } else {
-            while (at >= seq_first + G::seq_steps(a, q)) {  // on to the next sequence
-                seq_first += G::seq_steps(a, q);
-                ++u.s;
-                q = seq_info(a.b, a.pg, u.s);
-            }
-            u.steps = (int32_t)G::key_steps(q.keys);
-            const int64_t rows = (int64_t)q.len * a.group;
-            tiles = (int32_t)((rows + M - 1) / M);
-            const int64_t n = (at - seq_first) / u.steps;
-            u.first = seq_first + n * u.steps;
-            u.h = (int32_t)(n / tiles);
-            const int64_t r0 = (n % tiles) * M;
-            u.row0 = (int32_t)r0;
-            u.rows = (int32_t)(rows - r0 < M ? rows - r0 : M);
-            tok = q.start;
+            unit_of_step<KS, M>(a, at, u, q, seq_first);
         }
+        const int64_t tok = u.tok;  // the first token of its rows
         const int32_t step0 = (int32_t)(at - u.first);
         const int64_t unit_end = u.first + u.steps;
         const int32_t step1 = (int32_t)((end < unit_end ? end : unit_end) - u.first);
@@ -264,7 +150,7 @@ __global__ void __launch_bounds__(kBlock, workers_per_cu(D)) attention_kernel(At
         using KT = KeyTile<SUB, PAGE16>;
         auto locate = [&](int32_t step) {
             KT t;
-            const int32_t k0 = step * G::KS + wave * KW;
+            const int32_t k0 = step * KS + wave * KW;
             t.valid = 0;
             if constexpr (PAGE16) {
 #pragma unroll
@@ -318,7 +204,7 @@ __global__ void __launch_bounds__(kBlock, workers_per_cu(D)) attention_kernel(At
         // and the product with V, then the loads of the next V.
         while (more) {
             if constexpr (!QREG) asm volatile("" ::: "memory");  // queries are read anew from LDS
-            const int32_t k0 = step * G::KS + wave * KW;
+            const int32_t k0 = step * KS + wave * KW;
             const uint32_t valid = tile.valid;
             f32x4 x[R][SUB];
 #pragma unroll
@@ -455,29 +341,10 @@ __global__ void __launch_bounds__(kBlock, workers_per_cu(D)) attention_kernel(At
         __syncthreads();
         if (wave == 1) exchange(0, true);
         __syncthreads();
-        // Adds the infinities and NaN that the row's channels d.. have in the new tokens it looks at
-        // (of this part's steps) and that the products left out.
-        auto add_left_out = [&](int row, int d, float (&y)[T::CH]) {
-            const int64_t t = row_token(row);
-            const int32_t k1 = min((int64_t)q.keys, (int64_t)step1 * G::KS);
-            for (int32_t k = max(q.ctx, step0 * G::KS); k < k1; ++k) {
-                if (!(mask_bits(a, t, (int32_t)(t - q.start), k - q.ctx) & 1)) continue;
-                const int32_t slot = slot_of(a.pg, u.s, k);
-                if (slot < 0) continue;
-                const int64_t e0 = ((int64_t)slot * a.heads + u.h) * D + d;
-                for (int e = 0; e < T::CH; ++e) {
-                    const float f = cache_element<E, MX>(a.cache[1], a.scales[1], e0 + e);
-                    if ((__float_as_uint(f) & 0x7f800000u) == 0x7f800000u) y[e] += f;
-                }
-            }
-        };
         if (wave == 0) {
             exchange(0, false);
             const bool whole = step0 == 0 && step1 == u.steps;
-            // A part of a unit: slot 1 if it holds the unit's first step (the worker's last
-            // part), else slot 0 (its first).
-            float* part = reinterpret_cast<float*>(ws + a.part_offset) +
-                          ((int64_t)me * 2 + (step0 == 0 ? 1 : 0)) * (M * (D + 2));
+            float* part = part_of<M, D>(ws, a.part_offset, me, step0 == 0);
 #pragma unroll
             for (int r = 0; r < R; ++r) {
                 const int row = r * 16 + c;
@@ -502,7 +369,9 @@ __global__ void __launch_bounds__(kBlock, workers_per_cu(D)) attention_kernel(At
                         float y[T::CH];
 #pragma unroll
                         for (int e = 0; e < T::CH; ++e) y[e] = acc[r][v * T::CH + e][i] * inv;
-                        if (!SPARSE && left_out_any) add_left_out(row, d, y);
+                        if (!SPARSE && left_out_any)
+                            add_left_out<E, MX, D>(a, q, u, row_token(row), (int64_t)step0 * KS,
+                                                   (int64_t)step1 * KS, d, y);
                         if (whole) {
                             store_row<E, T::CH>(a.out, o + d, y);
                         } else {
@@ -517,80 +386,14 @@ __global__ void __launch_bounds__(kBlock, workers_per_cu(D)) attention_kernel(At
     }
 }
 
-// Joins the parts of the units that crossed workers: one wave per (token, query head).
-template <class E, bool MX, int D, int R, bool SPARSE>
-__global__ void __launch_bounds__(kBlock) join_kernel(AttnArgs a) {
-    using G = Geometry<E, MX, D, R, SPARSE>;
-    constexpr int kWorkers = workers(D);
-    constexpr int M = G::M;
-    constexpr int N = D / 64;
-    const int lane = threadIdx.x & 63;
-    const int64_t t = blockIdx.x;
-    const int hq = uniform((int)(blockIdx.y * kWaves + (threadIdx.x >> 6)));
-    if (hq >= a.heads * a.group) return;
-    const int s = seq_of_token(a.b, t);
-    const SeqInfo q = seq_info(a.b, a.pg, s);
-    const int64_t i = t - q.start;
-    if (i < 0 || i >= q.len) return;
-    const char* ws = static_cast<const char*>(a.ws);
-    const int h = hq / a.group;
-    int64_t first, total;
-    int32_t steps, row;
-    if constexpr (SPARSE) {
-        steps = G::block_steps(a);
-        const int32_t tiles = G::group_tiles(a);
-        row = hq - h * a.group;
-        first = ((t * a.heads + h) * tiles + row / M) * steps;
-        total = a.b.tokens * a.heads * tiles * steps;
-    } else {
-        const int64_t* prefix = reinterpret_cast<const int64_t*>(ws);
-        steps = (int32_t)G::key_steps(q.keys);
-        const int64_t tiles = ((int64_t)q.len * a.group + M - 1) / M;
-        row = (int32_t)(i * a.group + hq - h * a.group);
-        first = prefix[s] + (h * tiles + row / M) * steps;
-        total = prefix[a.b.num_seqs];
-    }
-    row %= M;
-    const Shares<kWorkers> sh(total);
-    const int32_t w0 = sh.owner(first), w1 = sh.owner(first + steps - 1);
-    if (w0 == w1) return;  // written by its worker
-    const float* parts = reinterpret_cast<const float*>(ws + a.part_offset);
-    auto part = [&](int32_t w) {
-        return parts + ((int64_t)w * 2 + (w == w0 ? 1 : 0)) * (M * (D + 2));
-    };
-    float big = -__builtin_inff();
-    for (int32_t w = w0; w <= w1; ++w) big = __builtin_fmaxf(big, part(w)[M * D + row]);
-    const float base = big == -__builtin_inff() ? 0.0f : big;
-    float sum = 0.0f, o[N];
-#pragma unroll
-    for (int j = 0; j < N; ++j) o[j] = 0.0f;
-    for (int32_t w = w0; w <= w1; ++w) {
-        const float* p = part(w);
-        const float f = exp2_fast(p[M * D + row] - base);
-        sum += p[M * D + M + row] * f;
-#pragma unroll
-        for (int j = 0; j < N; ++j)
-            o[j] = __builtin_fmaf(p[row * D + lane * N + j], f, o[j]);
-    }
-    const bool some = sum > 0.0f || sum != sum;
-    const float inv = some ? 1.0f / sum : 0.0f;
-#pragma unroll
-    for (int j = 0; j < N; ++j) o[j] *= inv;
-    const int64_t at = t * a.heads * a.group + hq;
-    store_row<E, N>(a.out, at * D + lane * N, o);
-    if (a.lse != nullptr && lane == 0)
-        a.lse[at] = some ? (big + log2_fast(sum)) * kLn2 : -__builtin_inff();
-}
-
 template <class E, bool MX, int D, int R, bool SPARSE>
 hipError_t run(const AttnArgs& a, hipStream_t st) {
     if (a.pg.shift >= 4) attention_kernel<E, MX, D, R, SPARSE, true><<<workers(D), kBlock, 0, st>>>(a);
     else attention_kernel<E, MX, D, R, SPARSE, false><<<workers(D), kBlock, 0, st>>>(a);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
-    const dim3 grid((uint32_t)a.b.tokens, (uint32_t)(a.heads * a.group + kWaves - 1) / kWaves);
-    join_kernel<E, MX, D, R, SPARSE><<<grid, kBlock, 0, st>>>(a);
-    return hipGetLastError();
+    constexpr int KS = 16 * Tile<E, MX, D>::SUB * kWaves;
+    return launch_join<E, D, KS, 16 * R, workers(D), SPARSE>(a, st);
 }
 
 template <class E, bool MX, int D, bool SPARSE>
@@ -614,13 +417,10 @@ hipError_t dispatch(const AttnArgs& a, bool mx, int dtype, int D, int R, hipStre
 
 }  // namespace
 
-hipError_t launch_tree_attention(const AttnArgs& a, bool mx, int dtype, int D, int R,
-                                 hipStream_t st) {
-    return dispatch<false>(a, mx, dtype, D, R, st);
-}
-hipError_t launch_block_attention(const AttnArgs& a, bool mx, int dtype, int D, int R,
-                                  hipStream_t st) {
-    return dispatch<true>(a, mx, dtype, D, R, st);
+hipError_t launch_attention(const AttnArgs& a, bool selected, bool mx, int dtype, int D, int R,
+                            hipStream_t st) {
+    return selected ? dispatch<true>(a, mx, dtype, D, R, st)
+                    : dispatch<false>(a, mx, dtype, D, R, st);
 }
 
 }  // namespace sc

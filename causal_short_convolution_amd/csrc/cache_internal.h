@@ -5,6 +5,7 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include "cache_attention.h"
 #include "shortconv_internal.h"
 
 namespace sc {
@@ -110,10 +111,10 @@ struct EvictArgs {
 
 hipError_t launch_verify_tree(const StepArgs& a, const VerifyArgs& va, const TreeArgs& ta,
                               bool mx, int dtype, int D, int W, hipStream_t stream);
-hipError_t launch_tree_attention(const AttnArgs& a, bool mx, int dtype, int D, int row_tiles,
+hipError_t launch_attention(const AttnArgs& a, bool selected, bool mx, int dtype, int D,
+                            int row_tiles, hipStream_t stream);
+hipError_t launch_wide_attention(const AttnArgs& a, bool mx, int D, AttnShape shape,
                                  hipStream_t stream);
-hipError_t launch_block_attention(const AttnArgs& a, bool mx, int dtype, int D, int row_tiles,
-                                  hipStream_t stream);
 hipError_t launch_cache_scores(const AttnArgs& a, bool mx, int dtype, int D, hipStream_t stream);
 hipError_t launch_block_summary(const SummaryArgs& a, bool mx, int dtype, int D,
                                 hipStream_t stream);

@@ -1,0 +1,406 @@
+// Tree attention for units of many query rows (shortconv_tree_attention, bf16 queries): the waves
+// share the keys and split the rows, 16 R rows each.
+//
+// With more than 32 rows the products outweigh the reads of the cache, and the waves of
+// cache_attention.hip, which each stream their own keys, would each hold all rows. Here a step of
+// 64 keys is brought in once per workgroup, into LDS in the form in which the products take it:
+// K by rows, V transposed (rows of channels, keys in the order in which the lane of a query row
+// holds their weights), both in bf16 whatever the cache holds. Two such buffers alternate: while
+// step t is computed from one, step t + 1, loaded to registers a step earlier, is written to the
+// other, and the loads of step t + 2 are under way. One barrier per step.
+//
+// LDS rows are padded by 16 bytes, and V's 16-byte groups of a row permuted by its channel / 16, so
+// that the 16 lanes that an LDS access serves at a time fall on different banks, both where
+// 4 keys x 8 channels are written and where 16 channels of 8 keys are read.
+#include <type_traits>
+
+#include "attention_line.h"
+
+namespace sc {
+namespace {
+
+constexpr int kKeys = 64;  // keys per step
+
+// Place of key group (kb, g) of channel d in V's LDS rows, in bytes; key groups are 8 keys: i, i + 16
+// for i = 32 kb + 4 g ..
+template <int D>
+struct Places {
+    static constexpr int KROW = D * 2 + 16;
+    static constexpr int VROW = kKeys * 2 + 16;
+    static constexpr int K_BYTES = kKeys * KROW;
+    static constexpr int V_BYTES = D * VROW;
+    __device__ static inline int v(int d, int kb, int g) {
+        return d * VROW + (((kb * 4 + g) ^ ((d >> 4) & 7)) << 4);
+    }
+};
+
+// What one thread loads of a step: pieces of K rows, and pieces of 4 rows of V.
+template <bool MX, int D, int NT>
+struct Pieces {
+    static constexpr int KP = MX ? D / 16 : D / 8;          // pieces of 16 bytes per K row
+    static constexpr int KN = (kKeys * KP + NT - 1) / NT;   // per thread
+    static constexpr int VP = D / 8;                        // pieces of 8 channels per V row
+    static constexpr int VN = (kKeys / 4 * VP + NT - 1) / NT;
+    uint4 k[KN];
+    uint32_t v[VN][4][MX ? 2 : 4];
+    uint8_t ks[MX ? KN : 1];
+    uint8_t vs[MX ? VN : 1][4];
+};
+
+template <bool MX, int D, int NW, int R>
+__global__ void __launch_bounds__(64 * NW, D == 256 && NW == 4 ? 1 : 2) wide_kernel(AttnArgs a) {
+    using T = Tile<BF16, false, D>;  // after staging the operands are bf16
+    using X = Tile<BF16, MX, D>;
+    using PL = Places<D>;
+    constexpr int NT = 64 * NW;
+    constexpr int M = 16 * R * NW;
+    constexpr int WORKERS = wide_workers(NW, D);
+    using PC = Pieces<MX, D, NT>;
+    __shared__ __attribute__((aligned(16))) char kbuf[2][PL::K_BYTES];
+    __shared__ __attribute__((aligned(16))) char vbuf[2][PL::V_BYTES];
+    __shared__ RunScratch run;
+    __shared__ int32_t left_out_any;
+
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int wave = uniform(tid >> 6);
+    const int c = lane & 15, g = lane >> 4;
+    constexpr int EB = MX ? 1 : 2;
+    const int64_t row_elems = (int64_t)a.heads * D;
+    char* ws = static_cast<char*>(a.ws);
+
+    const int64_t total = find_run<kKeys, M, WORKERS, NT>(a, reinterpret_cast<int64_t*>(ws), run);
+    const Shares<WORKERS> sh(total);
+    const int32_t me = sh.me();
+    if (me >= sh.workers) return;
+    int64_t at = sh.begin(me);
+    const int64_t end = sh.begin(me + 1);
+    Unit u;
+    u.s = uniform(run.s);
+    int64_t seq_first = uniform(run.first);
+    SeqInfo q = seq_info(a.b, a.pg, u.s);
+    const float to_log2 = a.scale * kLog2e;
+
+    while (at < end) {
+        unit_of_step<kKeys, M>(a, at, u, q, seq_first);
+        const int32_t step0 = (int32_t)(at - u.first);
+        const int64_t unit_end = u.first + u.steps;
+        const int32_t step1 = (int32_t)((end < unit_end ? end : unit_end) - u.first);
+        at = u.first + step1;
+
+        // Row tiles go round the waves: tile wave + NW r is the wave's r-th.
+        const int tiles = (u.rows + 15) / 16;
+        const int mine = tiles > wave ? (tiles - wave - 1) / NW + 1 : 0;
+        auto row_of = [&](int r) { return (wave + NW * r) * 16 + c; };
+        auto row_index = [&](int row) { return u.row0 + (row < u.rows ? row : u.rows - 1); };
+        typename T::Q qreg[R];
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            const int32_t x = row_index(row_of(r));
+            const int64_t off = (u.tok + x / a.group) * a.q_stride +
+                                (int64_t)(u.h * a.group + x % a.group) * D;
+            T::load_q(static_cast<const char*>(a.q) + off * 2, g, qreg[r]);
+        }
+        const char* kc = static_cast<const char*>(a.cache[0]) + (int64_t)u.h * D * EB;
+        const char* vc = static_cast<const char*>(a.cache[1]) + (int64_t)u.h * D * EB;
+        const uint8_t* ks = static_cast<const uint8_t*>(a.scales[0]) + u.h * (D / 32);
+        const uint8_t* vs = static_cast<const uint8_t*>(a.scales[1]) + u.h * (D / 32);
+
+        // ---- a step's keys: lane l finds the row of key l (-1: there is none)
+        auto find = [&](int32_t step) -> int32_t {
+            const int64_t p = (int64_t)step * kKeys + lane;
+            return step < step1 && p < q.keys ? slot_of(a.pg, u.s, (int32_t)p) : -1;
+        };
+        PC pc;
+        auto v_item = [&](int n, int& kb, int& gg, int& s, int& ch) {
+            const int x = n * NT + tid;
+            ch = x % PC::VP;
+            const int y = x / PC::VP;
+            s = y & 1;
+            gg = (y >> 1) & 3;
+            kb = y >> 3;
+            return kb < kKeys / 32;
+        };
+        auto load = [&](int32_t slots) {
+            const int32_t row = slots < 0 ? 0 : slots;
+#pragma unroll
+            for (int n = 0; n < PC::KN; ++n) {
+                const int x = n * NT + tid;
+                const int key = x / PC::KP, p = x % PC::KP;
+                const int64_t r = (int64_t)__shfl(row, key & 63) * row_elems;
+                if (kKeys * PC::KP % NT == 0 || key < kKeys) {
+                    pc.k[n] = *reinterpret_cast<const uint4*>(kc + r * EB + p * 16);
+                    if constexpr (MX) pc.ks[n] = ks[r / 32 + p / 2];
+                }
+            }
+#pragma unroll
+            for (int n = 0; n < PC::VN; ++n) {
+                int kb, gg, s, ch;
+                const bool in = v_item(n, kb, gg, s, ch);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const int key = (kb * 32 + s * 16 + gg * 4 + j) & 63;
+                    const int64_t r = (int64_t)__shfl(row, key) * row_elems;
+                    if (kKeys / 4 * PC::VP % NT == 0 || in) {
+                        const char* p = vc + r * EB + ch * 8 * EB;
+                        if constexpr (MX) {
+                            const uint2 w = *reinterpret_cast<const uint2*>(p);
+                            pc.v[n][j][0] = w.x;
+                            pc.v[n][j][1] = w.y;
+                            pc.vs[n][j] = vs[r / 32 + ch / 4];
+                        } else {
+                            const uint4 w = *reinterpret_cast<const uint4*>(p);
+                            pc.v[n][j][0] = w.x;
+                            pc.v[n][j][1] = w.y;
+                            pc.v[n][j][2] = w.z;
+                            pc.v[n][j][3] = w.w;
+                        }
+                    }
+                }
+            }
+        };
+        auto store = [&](int buf, int32_t step, uint64_t valid) {
+#pragma unroll
+            for (int n = 0; n < PC::KN; ++n) {
+                const int x = n * NT + tid;
+                const int key = x / PC::KP, p = x % PC::KP;
+                if (kKeys * PC::KP % NT == 0 || key < kKeys) {
+                    char* to = kbuf[buf] + key * PL::KROW;
+                    if constexpr (MX) {
+                        const float e = e8m0(pc.ks[n]);
+                        const uint32_t w[4] = {pc.k[n].x, pc.k[n].y, pc.k[n].z, pc.k[n].w};
+#pragma unroll
+                        for (int i = 0; i < 2; ++i)
+                            *reinterpret_cast<uint4*>(to + p * 32 + i * 16) = make_uint4(
+                                X::widen2(w[2 * i], e, false), X::widen2(w[2 * i], e, true),
+                                X::widen2(w[2 * i + 1], e, false), X::widen2(w[2 * i + 1], e, true));
+                    } else {
+                        *reinterpret_cast<uint4*>(to + p * 16) = pc.k[n];
+                    }
+                }
+            }
+            const bool plain = valid == ~0ull && (int64_t)(step + 1) * kKeys <= q.ctx;
+#pragma unroll
+            for (int n = 0; n < PC::VN; ++n) {
+                int kb, gg, s, ch;
+                const bool in = v_item(n, kb, gg, s, ch);
+                if (!(kKeys / 4 * PC::VP % NT == 0 || in)) continue;
+                uint32_t w[4][4];  // [key][channel pair]
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        if constexpr (MX)
+                            w[j][i] = X::widen2(pc.v[n][j][i / 2], e8m0(pc.vs[n][j]), i & 1);
+                        else
+                            w[j][i] = pc.v[n][j][i];
+                    }
+                if (!plain) {
+                    // Keys that do not exist count as zeros. Among the new tokens a row of V may be
+                    // one that only some query rows look at, and an infinity or a NaN times a weight
+                    // of zero would reach the others: those elements are left out here and added
+                    // at the end of the unit to the rows that do look at them.
+                    bool any = false;
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const bool ok = (valid >> (kb * 32 + s * 16 + gg * 4 + j)) & 1;
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const bool lo = (w[j][i] & 0x7f80u) == 0x7f80u;
+                            const bool hi = (w[j][i] & 0x7f800000u) == 0x7f800000u;
+                            any |= ok && (lo || hi);
+                            w[j][i] &= (lo ? 0xffff0000u : ~0u) & (hi ? 0x0000ffffu : ~0u);
+                            w[j][i] = ok ? w[j][i] : 0u;
+                        }
+                    }
+                    if (any) left_out_any = 1;
+                }
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    const uint32_t sel = (e & 1) ? 0x07060302u : 0x05040100u;
+                    const uint2 pair = make_uint2(
+                        __builtin_amdgcn_perm(w[1][e / 2], w[0][e / 2], sel),
+                        __builtin_amdgcn_perm(w[3][e / 2], w[2][e / 2], sel));
+                    *reinterpret_cast<uint2*>(vbuf[buf] + PL::v(ch * 8 + e, kb, gg) + s * 8) = pair;
+                }
+            }
+        };
+
+        float m[R], l[R];
+        f32x4 acc[R][T::NT];
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            m[r] = -__builtin_inff();
+            l[r] = 0.0f;
+#pragma unroll
+            for (int i = 0; i < T::NT; ++i) acc[r][i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+        }
+        // One step for the wave's first N row tiles.
+        auto compute = [&](auto count, int buf, int32_t step, uint64_t valid) {
+            constexpr int N = decltype(count)::value;
+            const int32_t k0 = step * kKeys;
+            f32x4 x[N][4];
+#pragma unroll
+            for (int s = 0; s < 4; ++s) {
+                typename T::KOp ko;
+#pragma unroll
+                for (int f = 0; f < T::NF; ++f)
+                    ko[f] = *reinterpret_cast<const bf16x8*>(kbuf[buf] + (s * 16 + c) * PL::KROW +
+                                                             f * 64 + g * 16);
+#pragma unroll
+                for (int r = 0; r < N; ++r) x[r][s] = T::logits(ko, qreg[r]);
+            }
+            const bool all_seen = valid == ~0ull && k0 + kKeys <= q.ctx;
+            bf16x8 p[N][2];
+#pragma unroll
+            for (int r = 0; r < N; ++r) {
+                float y[16];
+                float top = m[r];
+                uint32_t bits[2] = {(uint32_t)valid, (uint32_t)(valid >> 32)};
+                if (!all_seen) {
+                    const int32_t i = row_index(row_of(r)) / a.group;
+                    bits[0] &= mask_bits(a, u.tok + i, i, k0 - q.ctx);
+                    bits[1] &= mask_bits(a, u.tok + i, i, k0 + 32 - q.ctx);
+                }
+#pragma unroll
+                for (int j = 0; j < 16; ++j) {
+                    y[j] = x[r][j >> 2][j & 3] * to_log2;
+                    if (!all_seen) {
+                        const int key = (j >> 2 & 1) * 16 + (j & 3);
+                        y[j] = (bits[j >> 3] >> (key + g * 4)) & 1 ? y[j] : -__builtin_inff();
+                    }
+                    top = __builtin_fmaxf(top, y[j]);
+                }
+                top = row_max(top);
+                if (__ballot(top > m[r])) {  // rescale only when a maximum of the tile has moved
+                    const float base = top == -__builtin_inff() ? 0.0f : top;
+                    const float f = exp2_fast(m[r] - base);
+                    l[r] *= f;
+#pragma unroll
+                    for (int i = 0; i < T::NT; ++i)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) acc[r][i][e] *= f;
+                    m[r] = top;
+                }
+                const float base = m[r] == -__builtin_inff() ? 0.0f : m[r];
+#pragma unroll
+                for (int j = 0; j < 16; ++j) {
+                    y[j] = exp2_fast(y[j] - base);
+                    l[r] += y[j];
+                }
+#pragma unroll
+                for (int b = 0; b < 2; ++b)
+                    p[r][b] = __builtin_bit_cast(
+                        bf16x8, make_uint4(BF16::pack2(y[8 * b], y[8 * b + 1]),
+                                           BF16::pack2(y[8 * b + 2], y[8 * b + 3]),
+                                           BF16::pack2(y[8 * b + 4], y[8 * b + 5]),
+                                           BF16::pack2(y[8 * b + 6], y[8 * b + 7])));
+            }
+#pragma unroll
+            for (int n = 0; n < T::NT; ++n)
+#pragma unroll
+                for (int b = 0; b < 2; ++b) {
+                    const bf16x8 vo = *reinterpret_cast<const bf16x8*>(
+                        vbuf[buf] + PL::v(n * 16 + c, b, g));
+#pragma unroll
+                    for (int r = 0; r < N; ++r)
+                        acc[r][n] =
+                            __builtin_amdgcn_mfma_f32_16x16x32_bf16(vo, p[r][b], acc[r][n], 0, 0, 0);
+                }
+        };
+
+        __syncthreads();  // the last unit is done with LDS
+        if (tid == 0) left_out_any = 0;
+        int32_t slots = find(step0);
+        uint64_t now = __ballot(slots >= 0);
+        if (now) load(slots);
+        int32_t ahead = find(step0 + 1);
+        __syncthreads();  // left_out_any is cleared
+        if (now) store(0, step0, now);
+        uint64_t next = __ballot(ahead >= 0);
+        if (next) load(ahead);
+        ahead = find(step0 + 2);
+        __syncthreads();
+        for (int32_t step = step0; step < step1; ++step) {
+            const int buf = (step - step0) & 1;
+            if (next) store(buf ^ 1, step + 1, next);
+            const uint64_t after = __ballot(ahead >= 0);
+            if (after) load(ahead);
+            ahead = find(step + 3);
+            if (now && mine > 0) {
+                if (R == 1 || mine == R) compute(std::integral_constant<int, R>(), buf, step, now);
+                else compute(std::integral_constant<int, R == 1 ? 1 : R - 1>(), buf, step, now);
+            }
+            now = next;
+            next = after;
+            __syncthreads();
+        }
+
+        // ---- every wave writes its own rows
+        const bool whole = step0 == 0 && step1 == u.steps;
+        float* part = part_of<M, D>(ws, a.part_offset, me, step0 == 0);
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            const int row = row_of(r);
+            const float sum = row_sum(l[r]);
+            const bool some = sum > 0.0f || sum != sum;
+            const float inv = whole ? (some ? 1.0f / sum : 0.0f) : 1.0f;
+            if (row >= u.rows) continue;
+            const int32_t x = u.row0 + row;
+            const int64_t t = u.tok + x / a.group;
+            const int64_t o = t * a.heads * a.group + u.h * a.group + x % a.group;
+            if (g == 0) {
+                if (!whole) {
+                    part[M * D + row] = m[r];
+                    part[M * D + M + row] = sum;
+                } else if (a.lse != nullptr) {
+                    a.lse[o] = some ? (m[r] + log2_fast(sum)) * kLn2 : -__builtin_inff();
+                }
+            }
+#pragma unroll
+            for (int n = 0; n < T::NT; ++n) {
+                const int d = n * 16 + g * 4;
+                float y[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) y[e] = acc[r][n][e] * inv;
+                if (left_out_any)
+                    add_left_out<BF16, MX, D>(a, q, u, t, (int64_t)step0 * kKeys,
+                                              (int64_t)step1 * kKeys, d, y);
+                if (whole) store_row<BF16, 4>(a.out, o * D + d, y);
+                else *reinterpret_cast<f32x4*>(part + row * D + d) = f32x4{y[0], y[1], y[2], y[3]};
+            }
+        }
+    }
+}
+
+template <bool MX, int D, int NW, int R>
+hipError_t run(const AttnArgs& a, hipStream_t st) {
+    wide_kernel<MX, D, NW, R><<<wide_workers(NW, D), 64 * NW, 0, st>>>(a);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    return launch_join<BF16, D, kKeys, 16 * R * NW, wide_workers(NW, D), false>(a, st);
+}
+
+template <bool MX, int D>
+hipError_t by_shape(const AttnArgs& a, AttnShape s, hipStream_t st) {
+    if (s.waves == 4) return run<MX, D, 4, 1>(a, st);
+    if constexpr (D <= 128) {
+        if (s.tiles == 3) return run<MX, D, 8, 3>(a, st);
+        if (s.tiles == 2) return run<MX, D, 8, 2>(a, st);
+    }
+    return run<MX, D, 8, 1>(a, st);
+}
+
+template <bool MX>
+hipError_t by_dim(const AttnArgs& a, int D, AttnShape s, hipStream_t st) {
+    if (D == 64) return by_shape<MX, 64>(a, s, st);
+    if (D == 128) return by_shape<MX, 128>(a, s, st);
+    return by_shape<MX, 256>(a, s, st);
+}
+
+}  // namespace
+
+hipError_t launch_wide_attention(const AttnArgs& a, bool mx, int D, AttnShape s, hipStream_t st) {
+    return mx ? by_dim<true>(a, D, s, st) : by_dim<false>(a, D, s, st);
+}
+
+}  // namespace sc

@@ -144,8 +144,41 @@ def test_many_short_sequences():
                   drafts=[i % 3 for i in range(n)]))
 
 
-def test_many_rows_of_one_sequence():
-    check(Problem(14, "bf16", False, 1, 4, 64, 16, ctx=(150,), drafts=(130,), mask="tree"))
+@pytest.mark.parametrize("dtype,mx", KINDS)
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("G,drafts", [(3, (11, 0, 15)), (4, (16, 9)), (5, (20, 24)), (8, (33, 30)),
+                                      (16, (31, 1)), (7, (45, 60)), (20, (30,))])
+def test_rows_per_sequence(dtype, mx, D, G, drafts):
+    """From 33 to 600 query rows per sequence and cache head, over short and long contexts."""
+    check(Problem(14, dtype, mx, 2, G, D, 16, ctx=(150, 70, 1000)[:len(drafts)], drafts=drafts,
+                  mask="tree"))
+
+
+@pytest.mark.parametrize("bs", [1, 8, 64])
+@pytest.mark.parametrize("mask", [None, "random"])
+def test_many_rows_masks_and_pages(bs, mask):
+    check(Problem(22, "bf16", False, 1, 4, 128, bs, ctx=(150, 0, 63, 64), drafts=(20, 70, 9, 33),
+                  mask=mask, bad=0.2, behind=2))
+
+
+@pytest.mark.parametrize("what", [float("nan"), float("inf"), -float("inf")])
+def test_many_rows_masked_drafts_never_leak(what):
+    n = 24
+    mask = np.array([[(1 << i) | 1] if i != 3 else [0b1001] for i in range(n)], np.int64)
+    p = Problem(23, "bf16", False, 2, 4, 128, 16, ctx=(21,), drafts=(n,), mask=mask)
+    clean, clean_lse = run(p)
+    slot = int(p.table[0, 24 // 16]) * 16 + 24 % 16
+    for t in p.dev_kv:
+        t[slot] = what
+    out, lse = run(p)
+    rest = [i for i in range(n) if i != 3]
+    assert torch.equal(out[rest], clean[rest]) and torch.equal(lse[rest], clean_lse[rest])
+    assert not bool(torch.isfinite(out[3].float()).any())
+    p.dev_kv[0][slot] = 0.5  # a finite logit: what V holds is what comes out
+    out, lse = run(p)
+    assert torch.equal(out[rest], clean[rest])
+    got = out[3].float()
+    assert bool(got.isnan().all()) if what != what else bool((got == what).all())
 
 
 def test_cache_beyond_32_bit_offsets():
