@@ -148,21 +148,34 @@ __device__ inline float* part_of(void* ws, int64_t offset, int32_t worker, bool 
            ((int64_t)worker * 2 + holds_first) * (M * (D + 2));
 }
 
-// Adds to y (channels d.. of one row of token t) the infinities and NaN that V has in the new tokens
-// of key positions [k0, k1) that the row looks at, and that the products left out.
-template <class E, bool MX, int D, int N>
-__device__ inline void add_left_out(const AttnArgs& a, const SeqInfo& q, const Unit& u, int64_t t,
-                                    int64_t k0, int64_t k1, int d, float (&y)[N]) {
+// The infinities and NaN that V has in the new tokens of key positions [k0, k1), which the products
+// left out: adds them to the written rows (or part) of the unit that look at them. By the whole
+// workgroup, after the rows are written; rare.
+template <class E, bool MX, int D>
+__device__ inline void add_left_out(const AttnArgs& a, const SeqInfo& q, const Unit& u, int64_t k0,
+                                    int64_t k1, float* part) {
+    const int32_t first = (int32_t)max((int64_t)q.ctx, k0);
     const int32_t last = (int32_t)min((int64_t)q.keys, k1);
-    for (int32_t k = (int32_t)max((int64_t)q.ctx, k0); k < last; ++k) {
-        if (!(mask_bits(a, t, (int32_t)(t - q.start), k - q.ctx) & 1)) continue;
-        const int32_t slot = slot_of(a.pg, u.s, k);
-        if (slot < 0) continue;
-        const int64_t e0 = ((int64_t)slot * a.heads + u.h) * D + d;
-#pragma unroll
-        for (int e = 0; e < N; ++e) {
-            const float f = cache_element<E, MX>(a.cache[1], a.scales[1], e0 + e);
-            if ((__float_as_uint(f) & 0x7f800000u) == 0x7f800000u) y[e] += f;
+    for (int x = threadIdx.x; x < u.rows * D; x += blockDim.x) {
+        const int row = x / D, d = x % D;
+        const int32_t y = u.row0 + row, i = y / a.group;
+        const int64_t t = u.tok + i;
+        float extra = 0.0f;
+        for (int32_t k = first; k < last; ++k) {
+            if (!(mask_bits(a, t, i, k - q.ctx) & 1)) continue;
+            const int32_t slot = slot_of(a.pg, u.s, k);
+            if (slot < 0) continue;
+            const float f = cache_element<E, MX>(a.cache[1], a.scales[1],
+                                                 ((int64_t)slot * a.heads + u.h) * D + d);
+            if ((__float_as_uint(f) & 0x7f800000u) == 0x7f800000u) extra += f;
+        }
+        if (extra == 0.0f) continue;
+        if (part != nullptr) {
+            part[x] += extra;
+        } else {
+            const int64_t o = (t * a.heads * a.group + u.h * a.group + y % a.group) * D + d;
+            if constexpr (E::BYTES == 4) static_cast<float*>(a.out)[o] += extra;
+            else static_cast<__bf16*>(a.out)[o] = (__bf16)((float)static_cast<__bf16*>(a.out)[o] + extra);
         }
     }
 }
@@ -203,20 +216,43 @@ __global__ void __launch_bounds__(256) join_kernel(AttnArgs a) {
     const int32_t w0 = sh.owner(first), w1 = sh.owner(first + steps - 1);
     if (w0 == w1) return;  // written by its worker
     auto part = [&](int32_t w) { return part_of<M, D>(a.ws, a.part_offset, w, w == w0); };
+    // lane i takes the maximum and the sum of part w0 + i, 64 parts at a time
     float big = -__builtin_inff();
-    for (int32_t w = w0; w <= w1; ++w) big = __builtin_fmaxf(big, part(w)[M * D + row]);
+    for (int32_t w = w0 + lane; w <= w1; w += 64) big = __builtin_fmaxf(big, part(w)[M * D + row]);
+    for (int d = 1; d < 64; d <<= 1) big = __builtin_fmaxf(big, __shfl_xor(big, d));
     const float base = big == -__builtin_inff() ? 0.0f : big;
     float sum = 0.0f, o[N];
 #pragma unroll
     for (int j = 0; j < N; ++j) o[j] = 0.0f;
-    for (int32_t w = w0; w <= w1; ++w) {
-        const float* p = part(w);
-        const float f = exp2_fast(p[M * D + row] - base);
-        sum += p[M * D + M + row] * f;
+    for (int32_t v0 = w0; v0 <= w1; v0 += 64) {
+        const int n = min(64, w1 - v0 + 1);
+        float f = 0.0f;
+        if (lane < n) {
+            const float* p = part(v0 + lane);
+            f = exp2_fast(p[M * D + row] - base);
+            sum += p[M * D + M + row] * f;
+        }
+        constexpr int U = 4;  // rows in flight
+        for (int k = 0; k < n; k += U) {
+            float y[U][N];
 #pragma unroll
-        for (int j = 0; j < N; ++j)
-            o[j] = __builtin_fmaf(p[row * D + lane * N + j], f, o[j]);
+            for (int v = 0; v < U; ++v) {
+                const float* p = part(v0 + min(k + v, n - 1)) + row * D + lane * N;
+#pragma unroll
+                for (int j = 0; j < N; ++j) y[v][j] = p[j];
+            }
+#pragma unroll
+            for (int v = 0; v < U; ++v) {
+                const float fw = k + v < n ? __int_as_float(__builtin_amdgcn_readlane(
+                                                 __float_as_int(f), min(k + v, n - 1)))
+                                           : 0.0f;
+                if (k + v < n)
+#pragma unroll
+                    for (int j = 0; j < N; ++j) o[j] = __builtin_fmaf(y[v][j], fw, o[j]);
+            }
+        }
     }
+    for (int d = 1; d < 64; d <<= 1) sum += __shfl_xor(sum, d);
     const bool some = sum > 0.0f || sum != sum;
     const float inv = some ? 1.0f / sum : 0.0f;
 #pragma unroll

@@ -31,6 +31,29 @@ constexpr float kLn2 = 0.6931471805599453f;
 __device__ inline float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }
 __device__ inline float log2_fast(float x) { return __builtin_amdgcn_logf(x); }
 
+// Logits are q . k times a factor c > 0 in base 2 (a negative scale turns the queries' signs instead,
+// a scale of 0 clears them), so a row's running maximum is kept of the products alone and a
+// weight is one fused multiply-add and one exp2, 0 for a masked -inf. The reference value of a row, c
+// times its maximum; 0 while it has none.
+__device__ inline float logit_factor(float scale) {
+    return scale == 0.0f ? 1.0f : __builtin_fabsf(scale) * kLog2e;
+}
+__device__ inline float row_base(float top, float c) {
+    return top == -__builtin_inff() ? 0.0f : top * c;
+}
+// The maximum in base-2 logits, for joining parts.
+__device__ inline float row_top(float top, float c) {
+    return top == -__builtin_inff() ? top : top * c;
+}
+// A 16-byte piece of queries under the sign of the scale.
+template <class E>
+__device__ inline uint4 signed_by(uint4 x, float scale) {
+    const uint32_t turn = scale >= 0.0f ? 0u : E::BYTES == 2 ? 0x80008000u : 0x80000000u;
+    const uint32_t keep = scale == 0.0f ? 0u : 0xffffffffu;
+    return make_uint4((x.x ^ turn) & keep, (x.y ^ turn) & keep, (x.z ^ turn) & keep,
+                      (x.w ^ turn) & keep);
+}
+
 // Maximum and sum over the four lanes that hold one query row (lanes c, c + 16, c + 32, c + 48).
 __device__ inline float row_max(float v) {
     uint32_t u = __float_as_uint(v);

@@ -5,11 +5,9 @@
 
 namespace sc {
 
-// Workgroups that share out the steps, a multiple of the 8 XCDs: two on each of the 256 CUs, one
-// where a wave needs more than half of a SIMD's registers, or the workgroup more than half of
-// the CU's LDS or waves.
-constexpr int workers_per_cu(int head_dim) { return head_dim <= 128 ? 2 : 1; }
-constexpr int workers(int head_dim) { return 256 * workers_per_cu(head_dim); }
+// Workgroups that share out the steps, a multiple of the 8 XCDs: two on each of the 256 CUs; one
+// where the workgroup needs more than half of the CU's LDS or registers.
+constexpr int kWorkers = 512;
 constexpr int wide_workers(int waves, int head_dim) {
     return waves == 4 && head_dim <= 128 ? 512 : 256;
 }
@@ -22,15 +20,16 @@ struct AttnShape {
     int tiles;
     int rows() const { return 16 * tiles * (waves ? waves : 1); }
     int worker_count(int head_dim) const {
-        return waves ? wide_workers(waves, head_dim) : workers(head_dim);
+        return waves ? wide_workers(waves, head_dim) : kWorkers;
     }
 };
 
 // The shape for the rows of an average sequence (or token). Rows past a unit's make another unit,
 // which reads the keys again; rows that stay empty cost products and registers.
 inline AttnShape attention_shape(bool tree, int64_t rows, int element_bytes, int head_dim) {
-    if (rows <= 16) return {0, 1};
-    if (rows <= 32 || !tree || element_bytes == 4) return {0, 2};
+    const bool wide = tree && element_bytes == 2;
+    if (rows <= 16 || (head_dim > 128 && !wide)) return {0, 1};
+    if ((rows <= 32 && head_dim <= 128) || !wide) return {0, 2};
     if (rows <= 64) return {4, 1};
     if (rows <= 128 || head_dim > 128) return {8, 1};
     return rows > 256 && rows <= 384 ? AttnShape{8, 3} : AttnShape{8, 2};

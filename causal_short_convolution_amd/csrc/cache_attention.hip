@@ -20,9 +20,9 @@ constexpr int kBlock = 256;
 constexpr int kWaves = 4;
 
 template <class E, bool MX, int D, int R, bool SPARSE, bool PAGE16>
-__global__ void __launch_bounds__(kBlock, workers_per_cu(D)) attention_kernel(AttnArgs a) {
+__global__ void __launch_bounds__(kBlock, 2) attention_kernel(AttnArgs a) {
     using T = Tile<E, MX, D>;
-    constexpr int WORKERS = workers(D);
+    constexpr int WORKERS = kWorkers;
     constexpr int M = 16 * R;
     constexpr int SUB = T::SUB;
     constexpr int KW = 16 * SUB;      // keys per wave and step
@@ -30,6 +30,7 @@ __global__ void __launch_bounds__(kBlock, workers_per_cu(D)) attention_kernel(At
     constexpr uint32_t kFull = SUB == 2 ? 0xffffffffu : 0xffffu;
     constexpr int QSTRIDE = D * T::QB + 16;  // query rows in LDS, staggered over the banks
     constexpr bool QREG = R == 1 && D <= 128;  // query operands stay in registers
+    constexpr bool AHEAD = R == 1 && D <= 128; // keys are loaded a step ahead
     constexpr int OSTRIDE = D + 4;           // output rows in LDS (floats)
     constexpr int kLds = 2 * M * OSTRIDE * 4 > M * QSTRIDE ? 2 * M * OSTRIDE * 4 : M * QSTRIDE;
     __shared__ __attribute__((aligned(16))) char lds[kLds];
@@ -113,8 +114,8 @@ __global__ void __launch_bounds__(kBlock, workers_per_cu(D)) attention_kernel(At
             for (int x = tid; x < M * PIECES; x += kBlock) {
                 const int r = x / PIECES, p = x % PIECES;
                 const int64_t off = row_token(r) * a.q_stride + (int64_t)row_head(r) * D;
-                *reinterpret_cast<uint4*>(lds + r * QSTRIDE + p * 16) =
-                    *reinterpret_cast<const uint4*>(qb + off * T::QB + p * 16);
+                *reinterpret_cast<uint4*>(lds + r * QSTRIDE + p * 16) = signed_by<E>(
+                    *reinterpret_cast<const uint4*>(qb + off * T::QB + p * 16), a.scale);
             }
         }
         __syncthreads();
@@ -182,7 +183,7 @@ __global__ void __launch_bounds__(kBlock, workers_per_cu(D)) attention_kernel(At
 #pragma unroll
             for (int i = 0; i < T::NT; ++i) acc[r][i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
         }
-        const float to_log2 = a.scale * kLog2e;
+        const float to_log2 = logit_factor(a.scale);
         typename T::K kreg;
         typename T::V vreg;
         auto next_tile = [&](int32_t& step, KT& t) {  // the next step from `step` on with a key
@@ -196,14 +197,21 @@ __global__ void __launch_bounds__(kBlock, workers_per_cu(D)) attention_kernel(At
         int32_t step = step0;
         KT tile;
         bool more = next_tile(step, tile);
-        if (more) {
-            T::load_k(kc, ks, tile, row_bytes, c, g, kreg);
-            T::load_v(vc, vs, tile, row_bytes, c, g, vreg);
+        auto load_keys = [&](const KT& t) { T::load_k(kc, ks, t, row_bytes, c, g, kreg); };
+        auto load_values = [&](const KT& t) { T::load_v(vc, vs, t, row_bytes, c, g, vreg); };
+        if (AHEAD && more) {
+            load_keys(tile);
+            load_values(tile);
         }
         // Per step: logits from K, then the loads of the next K into the same registers, softmax
-        // and the product with V, then the loads of the next V.
+        // and the product with V, then the loads of the next V. Where that takes more than half of
+        // a SIMD's registers a step loads its own keys, and the other waves cover the wait.
         while (more) {
             if constexpr (!QREG) asm volatile("" ::: "memory");  // queries are read anew from LDS
+            if constexpr (!AHEAD) {
+                load_keys(tile);
+                load_values(tile);
+            }
             const int32_t k0 = step * KS + wave * KW;
             const uint32_t valid = tile.valid;
             f32x4 x[R][SUB];
@@ -225,7 +233,7 @@ __global__ void __launch_bounds__(kBlock, workers_per_cu(D)) attention_kernel(At
             KT next;
             int32_t next_step = step + 1;
             const bool another = next_tile(next_step, next);
-            if (another) T::load_k(kc, ks, next, row_bytes, c, g, kreg);
+            if (AHEAD && another) load_keys(next);
 
             // Which keys a row looks at. Every key of a full step below the context is seen by all
             // rows; selected pages are one token's, seen alike by all its heads.
@@ -240,28 +248,31 @@ __global__ void __launch_bounds__(kBlock, workers_per_cu(D)) attention_kernel(At
                 if (valid != kFull) T::clear(vo, valid, g);
                 if (!SPARSE && T::cleanse(vo)) left_out = 1;
             }
+            if (!all_seen) {
+#pragma unroll
+                for (int r = 0; r < R; ++r) {
+                    uint32_t bits = valid;
+                    if constexpr (!SPARSE) {
+                        const int64_t t = row_token(r * 16 + c);
+                        bits &= mask_bits(a, t, (int32_t)(t - q.start), k0 - q.ctx);
+                    }
+                    bits >>= g * 4;
+#pragma unroll
+                    for (int j = 0; j < SUB * 4; ++j)
+                        if (!((bits >> ((j >> 2) * 16 + (j & 3))) & 1))
+                            x[r][j >> 2][j & 3] = -__builtin_inff();
+                }
+            }
 #pragma unroll
             for (int r = 0; r < R; ++r) {
                 float p[SUB * 4];
                 float top = m[r];
-                uint32_t bits = valid;
-                if (!SPARSE && !all_seen) {
-                    const int64_t t = row_token(r * 16 + c);
-                    bits &= mask_bits(a, t, (int32_t)(t - q.start), k0 - q.ctx);
-                }
 #pragma unroll
-                for (int j = 0; j < SUB * 4; ++j) {
-                    p[j] = x[r][j >> 2][j & 3] * to_log2;
-                    if (!all_seen) {
-                        const bool see = (bits >> ((j >> 2) * 16 + g * 4 + (j & 3))) & 1;
-                        p[j] = see ? p[j] : -__builtin_inff();
-                    }
-                    top = __builtin_fmaxf(top, p[j]);
-                }
+                for (int j = 0; j < SUB * 4; ++j)
+                    top = __builtin_fmaxf(top, x[r][j >> 2][j & 3]);
                 top = row_max(top);
-                if (__ballot(top > m[r])) {  // rescale only when a maximum of the tile has moved
-                    const float base = top == -__builtin_inff() ? 0.0f : top;
-                    const float f = exp2_fast(m[r] - base);
+                if (__ballot(top > m[r])) {  // rescale only when a maximum has moved
+                    const float f = exp2_fast(row_top(m[r], to_log2) - row_base(top, to_log2));
                     l[r] *= f;
 #pragma unroll
                     for (int i = 0; i < T::NT; ++i)
@@ -269,15 +280,15 @@ __global__ void __launch_bounds__(kBlock, workers_per_cu(D)) attention_kernel(At
                         for (int e = 0; e < 4; ++e) acc[r][i][e] *= f;
                     m[r] = top;
                 }
-                const float base = m[r] == -__builtin_inff() ? 0.0f : m[r];
+                const float base = row_base(m[r], to_log2);
 #pragma unroll
                 for (int j = 0; j < SUB * 4; ++j) {
-                    p[j] = exp2_fast(p[j] - base);
+                    p[j] = exp2_fast(__builtin_fmaf(x[r][j >> 2][j & 3], to_log2, -base));
                     l[r] += p[j];
                 }
                 T::values(vo, p, acc[r]);
             }
-            if (another) T::load_v(vc, vs, next, row_bytes, c, g, vreg);
+            if (AHEAD && another) load_values(next);
             more = another;
             step = next_step;
             tile = next;
@@ -289,6 +300,7 @@ __global__ void __launch_bounds__(kBlock, workers_per_cu(D)) attention_kernel(At
 #pragma unroll
         for (int r = 0; r < R; ++r) {
             l[r] = row_sum(l[r]);
+            m[r] = row_top(m[r], to_log2);  // from here on in base-2 logits
             if (g == 0) {
                 stat[wave][0][r * 16 + c] = m[r];
                 stat[wave][1][r * 16 + c] = l[r];
@@ -341,10 +353,10 @@ __global__ void __launch_bounds__(kBlock, workers_per_cu(D)) attention_kernel(At
         __syncthreads();
         if (wave == 1) exchange(0, true);
         __syncthreads();
+        const bool whole = step0 == 0 && step1 == u.steps;
+        float* part = part_of<M, D>(ws, a.part_offset, me, step0 == 0);
         if (wave == 0) {
             exchange(0, false);
-            const bool whole = step0 == 0 && step1 == u.steps;
-            float* part = part_of<M, D>(ws, a.part_offset, me, step0 == 0);
 #pragma unroll
             for (int r = 0; r < R; ++r) {
                 const int row = r * 16 + c;
@@ -369,9 +381,6 @@ __global__ void __launch_bounds__(kBlock, workers_per_cu(D)) attention_kernel(At
                         float y[T::CH];
 #pragma unroll
                         for (int e = 0; e < T::CH; ++e) y[e] = acc[r][v * T::CH + e][i] * inv;
-                        if (!SPARSE && left_out_any)
-                            add_left_out<E, MX, D>(a, q, u, row_token(row), (int64_t)step0 * KS,
-                                                   (int64_t)step1 * KS, d, y);
                         if (whole) {
                             store_row<E, T::CH>(a.out, o + d, y);
                         } else {
@@ -383,22 +392,30 @@ __global__ void __launch_bounds__(kBlock, workers_per_cu(D)) attention_kernel(At
                     }
             }
         }
+        if (!SPARSE && left_out_any) {  // (set before the waves met, the same for all)
+            __syncthreads();            // the rows are written
+            add_left_out<E, MX, D>(a, q, u, (int64_t)step0 * KS, (int64_t)step1 * KS,
+                                   whole ? nullptr : part);
+        }
     }
 }
 
 template <class E, bool MX, int D, int R, bool SPARSE>
 hipError_t run(const AttnArgs& a, hipStream_t st) {
-    if (a.pg.shift >= 4) attention_kernel<E, MX, D, R, SPARSE, true><<<workers(D), kBlock, 0, st>>>(a);
-    else attention_kernel<E, MX, D, R, SPARSE, false><<<workers(D), kBlock, 0, st>>>(a);
+    if (a.pg.shift >= 4) attention_kernel<E, MX, D, R, SPARSE, true><<<kWorkers, kBlock, 0, st>>>(a);
+    else attention_kernel<E, MX, D, R, SPARSE, false><<<kWorkers, kBlock, 0, st>>>(a);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
     constexpr int KS = 16 * Tile<E, MX, D>::SUB * kWaves;
-    return launch_join<E, D, KS, 16 * R, workers(D), SPARSE>(a, st);
+    return launch_join<E, D, KS, 16 * R, kWorkers, SPARSE>(a, st);
 }
 
 template <class E, bool MX, int D, bool SPARSE>
 hipError_t by_rows(const AttnArgs& a, int R, hipStream_t st) {
-    return R == 1 ? run<E, MX, D, 1, SPARSE>(a, st) : run<E, MX, D, 2, SPARSE>(a, st);
+    if constexpr (D <= 128) {
+        if (R == 2) return run<E, MX, D, 2, SPARSE>(a, st);
+    }
+    return run<E, MX, D, 1, SPARSE>(a, st);
 }
 
 template <class E, bool MX, bool SPARSE>

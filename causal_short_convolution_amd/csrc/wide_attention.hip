@@ -9,29 +9,25 @@
 // step t is computed from one, step t + 1, loaded to registers a step earlier, is written to the
 // other, and the loads of step t + 2 are under way. One barrier per step.
 //
-// LDS rows are padded by 16 bytes, and V's 16-byte groups of a row permuted by its channel / 16, so
-// that the 16 lanes that an LDS access serves at a time fall on different banks, both where
-// 4 keys x 8 channels are written and where 16 channels of 8 keys are read.
-#include <type_traits>
-
+// LDS rows are padded by 16 bytes, and the row of channel CW c + e of V (CW = 8, for heads of 64 4) is
+// e D / CW + c, so that the lanes that an LDS access serves at a time fall on different banks both
+// where CW channels of 4 keys are written and where 16 rows of 8 keys are read.
 #include "attention_line.h"
 
 namespace sc {
 namespace {
 
 constexpr int kKeys = 64;  // keys per step
+constexpr int kNoLds = 0x7f;  // scheduling barrier that everything but LDS accesses may cross
 
-// Place of key group (kb, g) of channel d in V's LDS rows, in bytes; key groups are 8 keys: i, i + 16
-// for i = 32 kb + 4 g ..
 template <int D>
 struct Places {
     static constexpr int KROW = D * 2 + 16;
     static constexpr int VROW = kKeys * 2 + 16;
     static constexpr int K_BYTES = kKeys * KROW;
     static constexpr int V_BYTES = D * VROW;
-    __device__ static inline int v(int d, int kb, int g) {
-        return d * VROW + (((kb * 4 + g) ^ ((d >> 4) & 7)) << 4);
-    }
+    static constexpr int CW = D / 16 < 8 ? D / 16 : 8;  // channels that a thread turns at a time
+    __device__ static inline int v_row(int c, int e) { return e * (D / CW) + c; }
 };
 
 // What one thread loads of a step: pieces of K rows, and pieces of 4 rows of V.
@@ -39,10 +35,11 @@ template <bool MX, int D, int NT>
 struct Pieces {
     static constexpr int KP = MX ? D / 16 : D / 8;          // pieces of 16 bytes per K row
     static constexpr int KN = (kKeys * KP + NT - 1) / NT;   // per thread
-    static constexpr int VP = D / 8;                        // pieces of 8 channels per V row
+    static constexpr int CW = Places<D>::CW;
+    static constexpr int VP = D / CW;                       // pieces of CW channels per V row
     static constexpr int VN = (kKeys / 4 * VP + NT - 1) / NT;
     uint4 k[KN];
-    uint32_t v[VN][4][MX ? 2 : 4];
+    uint32_t v[VN][4][MX ? CW / 4 : CW / 2];
     uint8_t ks[MX ? KN : 1];
     uint8_t vs[MX ? VN : 1][4];
 };
@@ -78,7 +75,7 @@ __global__ void __launch_bounds__(64 * NW, D == 256 && NW == 4 ? 1 : 2) wide_ker
     u.s = uniform(run.s);
     int64_t seq_first = uniform(run.first);
     SeqInfo q = seq_info(a.b, a.pg, u.s);
-    const float to_log2 = a.scale * kLog2e;
+    const float to_log2 = logit_factor(a.scale);
 
     while (at < end) {
         unit_of_step<kKeys, M>(a, at, u, q, seq_first);
@@ -99,16 +96,28 @@ __global__ void __launch_bounds__(64 * NW, D == 256 && NW == 4 ? 1 : 2) wide_ker
             const int64_t off = (u.tok + x / a.group) * a.q_stride +
                                 (int64_t)(u.h * a.group + x % a.group) * D;
             T::load_q(static_cast<const char*>(a.q) + off * 2, g, qreg[r]);
+#pragma unroll
+            for (int f = 0; f < T::NF; ++f)
+                qreg[r][f] = __builtin_bit_cast(
+                    bf16x8, signed_by<BF16>(__builtin_bit_cast(uint4, qreg[r][f]), a.scale));
         }
         const char* kc = static_cast<const char*>(a.cache[0]) + (int64_t)u.h * D * EB;
         const char* vc = static_cast<const char*>(a.cache[1]) + (int64_t)u.h * D * EB;
         const uint8_t* ks = static_cast<const uint8_t*>(a.scales[0]) + u.h * (D / 32);
         const uint8_t* vs = static_cast<const uint8_t*>(a.scales[1]) + u.h * (D / 32);
 
-        // ---- a step's keys: lane l finds the row of key l (-1: there is none)
-        auto find = [&](int32_t step) -> int32_t {
+        // ---- a step's keys: lane l finds the row of key l (-1: there is none). The page id is
+        // fetched a step before it is looked at, so that nothing waits for it.
+        const int32_t* table = a.pg.table + (int64_t)u.s * a.pg.max_blocks;
+        const int32_t last = q.keys > 0 ? q.keys - 1 : 0;
+        auto fetch = [&](int32_t step) -> int32_t {
             const int64_t p = (int64_t)step * kKeys + lane;
-            return step < step1 && p < q.keys ? slot_of(a.pg, u.s, (int32_t)p) : -1;
+            return q.keys > 0 ? table[(int32_t)min(p, (int64_t)last) >> a.pg.shift] : -1;
+        };
+        auto row_slot = [&](int32_t page, int32_t step) -> int32_t {
+            const int64_t p = (int64_t)step * kKeys + lane;
+            const bool ok = step < step1 && p < q.keys && page >= 0 && page < a.pg.num_pages;
+            return ok ? (page << a.pg.shift) + ((int32_t)p & ((1 << a.pg.shift) - 1)) : -1;
         };
         PC pc;
         auto v_item = [&](int n, int& kb, int& gg, int& s, int& ch) {
@@ -141,19 +150,22 @@ __global__ void __launch_bounds__(64 * NW, D == 256 && NW == 4 ? 1 : 2) wide_ker
                     const int key = (kb * 32 + s * 16 + gg * 4 + j) & 63;
                     const int64_t r = (int64_t)__shfl(row, key) * row_elems;
                     if (kKeys / 4 * PC::VP % NT == 0 || in) {
-                        const char* p = vc + r * EB + ch * 8 * EB;
-                        if constexpr (MX) {
-                            const uint2 w = *reinterpret_cast<const uint2*>(p);
-                            pc.v[n][j][0] = w.x;
-                            pc.v[n][j][1] = w.y;
-                            pc.vs[n][j] = vs[r / 32 + ch / 4];
+                        const char* p = vc + r * EB + ch * PL::CW * EB;
+                        uint32_t(&w)[MX ? PL::CW / 4 : PL::CW / 2] = pc.v[n][j];
+                        if constexpr (PL::CW * EB == 16) {
+                            const uint4 x = *reinterpret_cast<const uint4*>(p);
+                            w[0] = x.x;
+                            w[1] = x.y;
+                            w[2] = x.z;
+                            w[3] = x.w;
+                        } else if constexpr (PL::CW * EB == 8) {
+                            const uint2 x = *reinterpret_cast<const uint2*>(p);
+                            w[0] = x.x;
+                            w[1] = x.y;
                         } else {
-                            const uint4 w = *reinterpret_cast<const uint4*>(p);
-                            pc.v[n][j][0] = w.x;
-                            pc.v[n][j][1] = w.y;
-                            pc.v[n][j][2] = w.z;
-                            pc.v[n][j][3] = w.w;
+                            w[0] = *reinterpret_cast<const uint32_t*>(p);
                         }
+                        if constexpr (MX) pc.vs[n][j] = vs[r / 32 + ch * PL::CW / 32];
                     }
                 }
             }
@@ -184,11 +196,12 @@ __global__ void __launch_bounds__(64 * NW, D == 256 && NW == 4 ? 1 : 2) wide_ker
                 int kb, gg, s, ch;
                 const bool in = v_item(n, kb, gg, s, ch);
                 if (!(kKeys / 4 * PC::VP % NT == 0 || in)) continue;
-                uint32_t w[4][4];  // [key][channel pair]
+                constexpr int CP = PL::CW / 2;
+                uint32_t w[4][CP];  // [key][channel pair]
 #pragma unroll
                 for (int j = 0; j < 4; ++j)
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
+                    for (int i = 0; i < CP; ++i) {
                         if constexpr (MX)
                             w[j][i] = X::widen2(pc.v[n][j][i / 2], e8m0(pc.vs[n][j]), i & 1);
                         else
@@ -204,7 +217,7 @@ __global__ void __launch_bounds__(64 * NW, D == 256 && NW == 4 ? 1 : 2) wide_ker
                     for (int j = 0; j < 4; ++j) {
                         const bool ok = (valid >> (kb * 32 + s * 16 + gg * 4 + j)) & 1;
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) {
+                        for (int i = 0; i < CP; ++i) {
                             const bool lo = (w[j][i] & 0x7f80u) == 0x7f80u;
                             const bool hi = (w[j][i] & 0x7f800000u) == 0x7f800000u;
                             any |= ok && (lo || hi);
@@ -215,12 +228,14 @@ __global__ void __launch_bounds__(64 * NW, D == 256 && NW == 4 ? 1 : 2) wide_ker
                     if (any) left_out_any = 1;
                 }
 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
+                for (int e = 0; e < PL::CW; ++e) {
                     const uint32_t sel = (e & 1) ? 0x07060302u : 0x05040100u;
                     const uint2 pair = make_uint2(
                         __builtin_amdgcn_perm(w[1][e / 2], w[0][e / 2], sel),
                         __builtin_amdgcn_perm(w[3][e / 2], w[2][e / 2], sel));
-                    *reinterpret_cast<uint2*>(vbuf[buf] + PL::v(ch * 8 + e, kb, gg) + s * 8) = pair;
+                    // keys i, i + 16 for i = 32 kb + 4 g .. share a group of 16 bytes
+                    *reinterpret_cast<uint2*>(vbuf[buf] + PL::v_row(ch, e) * PL::VROW +
+                                              (kb * 4 + gg) * 16 + s * 8) = pair;
                 }
             }
         };
@@ -234,46 +249,67 @@ __global__ void __launch_bounds__(64 * NW, D == 256 && NW == 4 ? 1 : 2) wide_ker
 #pragma unroll
             for (int i = 0; i < T::NT; ++i) acc[r][i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
         }
-        // One step for the wave's first N row tiles.
-        auto compute = [&](auto count, int buf, int32_t step, uint64_t valid) {
-            constexpr int N = decltype(count)::value;
+        // One step for the wave's row tiles. LDS is read AHEAD operands ahead of
+        // the products that take them (the barriers keep LDS reads where they are written).
+        auto compute = [&](int buf, int32_t step, uint64_t valid) {
             const int32_t k0 = step * kKeys;
-            f32x4 x[N][4];
+            const char* kb = kbuf[buf] + c * PL::KROW + g * 16;
+            const char* vb = vbuf[buf] + c * PL::VROW + g * 16;
+            // operand i of K: subtile i / NF, channels f = i % NF; of V: channel tile i / 2, keys 32 (i % 2)
+            constexpr int AHEAD = 4;
+            constexpr int NK = 4 * T::NF, NV = 2 * T::NT;
+            bf16x8 op[AHEAD];
+            auto read_k = [&](int i) {
+                op[i % AHEAD] = *reinterpret_cast<const bf16x8*>(kb + i / T::NF * 16 * PL::KROW +
+                                                                 i % T::NF * 64);
+            };
+            auto read_v = [&](int i) {
+                op[i % AHEAD] = *reinterpret_cast<const bf16x8*>(vb + i / 2 * 16 * PL::VROW +
+                                                                 i % 2 * 64);
+            };
+            f32x4 x[R][4];
 #pragma unroll
-            for (int s = 0; s < 4; ++s) {
-                typename T::KOp ko;
+            for (int r = 0; r < R; ++r)
 #pragma unroll
-                for (int f = 0; f < T::NF; ++f)
-                    ko[f] = *reinterpret_cast<const bf16x8*>(kbuf[buf] + (s * 16 + c) * PL::KROW +
-                                                             f * 64 + g * 16);
+                for (int s = 0; s < 4; ++s) x[r][s] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-                for (int r = 0; r < N; ++r) x[r][s] = T::logits(ko, qreg[r]);
+            for (int i = 0; i < AHEAD; ++i) read_k(i);
+#pragma unroll
+            for (int i = 0; i < NK; ++i) {
+#pragma unroll
+                for (int r = 0; r < R; ++r)
+                    x[r][i / T::NF] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+                        op[i % AHEAD], qreg[r][i % T::NF], x[r][i / T::NF], 0, 0, 0);
+                if (i + AHEAD < NK) read_k(i + AHEAD);
+                __builtin_amdgcn_sched_barrier(kNoLds);
             }
-            const bool all_seen = valid == ~0ull && k0 + kKeys <= q.ctx;
-            bf16x8 p[N][2];
+            if (valid != ~0ull || k0 + kKeys > q.ctx) {  // some rows do not look at some keys
 #pragma unroll
-            for (int r = 0; r < N; ++r) {
+                for (int r = 0; r < R; ++r) {
+                    const int32_t i = row_index(row_of(r)) / a.group;
+                    const uint32_t bits[2] = {
+                        ((uint32_t)valid & mask_bits(a, u.tok + i, i, k0 - q.ctx)) >> (g * 4),
+                        ((uint32_t)(valid >> 32) & mask_bits(a, u.tok + i, i, k0 + 32 - q.ctx)) >>
+                            (g * 4)};
+#pragma unroll
+                    for (int j = 0; j < 16; ++j)
+                        if (!((bits[j >> 3] >> ((j >> 2 & 1) * 16 + (j & 3))) & 1))
+                            x[r][j >> 2][j & 3] = -__builtin_inff();
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < AHEAD; ++i) read_v(i);
+            __builtin_amdgcn_sched_barrier(kNoLds);
+            bf16x8 p[R][2];
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
                 float y[16];
                 float top = m[r];
-                uint32_t bits[2] = {(uint32_t)valid, (uint32_t)(valid >> 32)};
-                if (!all_seen) {
-                    const int32_t i = row_index(row_of(r)) / a.group;
-                    bits[0] &= mask_bits(a, u.tok + i, i, k0 - q.ctx);
-                    bits[1] &= mask_bits(a, u.tok + i, i, k0 + 32 - q.ctx);
-                }
 #pragma unroll
-                for (int j = 0; j < 16; ++j) {
-                    y[j] = x[r][j >> 2][j & 3] * to_log2;
-                    if (!all_seen) {
-                        const int key = (j >> 2 & 1) * 16 + (j & 3);
-                        y[j] = (bits[j >> 3] >> (key + g * 4)) & 1 ? y[j] : -__builtin_inff();
-                    }
-                    top = __builtin_fmaxf(top, y[j]);
-                }
+                for (int j = 0; j < 16; ++j) top = __builtin_fmaxf(top, x[r][j >> 2][j & 3]);
                 top = row_max(top);
-                if (__ballot(top > m[r])) {  // rescale only when a maximum of the tile has moved
-                    const float base = top == -__builtin_inff() ? 0.0f : top;
-                    const float f = exp2_fast(m[r] - base);
+                if (__ballot(top > m[r])) {  // rescale only when a maximum has moved
+                    const float f = exp2_fast(row_top(m[r], to_log2) - row_base(top, to_log2));
                     l[r] *= f;
 #pragma unroll
                     for (int i = 0; i < T::NT; ++i)
@@ -281,10 +317,10 @@ __global__ void __launch_bounds__(64 * NW, D == 256 && NW == 4 ? 1 : 2) wide_ker
                         for (int e = 0; e < 4; ++e) acc[r][i][e] *= f;
                     m[r] = top;
                 }
-                const float base = m[r] == -__builtin_inff() ? 0.0f : m[r];
+                const float base = row_base(m[r], to_log2);
 #pragma unroll
                 for (int j = 0; j < 16; ++j) {
-                    y[j] = exp2_fast(y[j] - base);
+                    y[j] = exp2_fast(__builtin_fmaf(x[r][j >> 2][j & 3], to_log2, -base));
                     l[r] += y[j];
                 }
 #pragma unroll
@@ -296,40 +332,36 @@ __global__ void __launch_bounds__(64 * NW, D == 256 && NW == 4 ? 1 : 2) wide_ker
                                            BF16::pack2(y[8 * b + 6], y[8 * b + 7])));
             }
 #pragma unroll
-            for (int n = 0; n < T::NT; ++n)
+            for (int i = 0; i < NV; ++i) {
 #pragma unroll
-                for (int b = 0; b < 2; ++b) {
-                    const bf16x8 vo = *reinterpret_cast<const bf16x8*>(
-                        vbuf[buf] + PL::v(n * 16 + c, b, g));
-#pragma unroll
-                    for (int r = 0; r < N; ++r)
-                        acc[r][n] =
-                            __builtin_amdgcn_mfma_f32_16x16x32_bf16(vo, p[r][b], acc[r][n], 0, 0, 0);
-                }
+                for (int r = 0; r < R; ++r)
+                    acc[r][i / 2] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+                        op[i % AHEAD], p[r][i % 2], acc[r][i / 2], 0, 0, 0);
+                if (i + AHEAD < NV) read_v(i + AHEAD);
+                __builtin_amdgcn_sched_barrier(kNoLds);
+            }
         };
-
         __syncthreads();  // the last unit is done with LDS
         if (tid == 0) left_out_any = 0;
-        int32_t slots = find(step0);
+        int32_t slots = row_slot(fetch(step0), step0);
+        int32_t page = fetch(step0 + 1);
         uint64_t now = __ballot(slots >= 0);
         if (now) load(slots);
-        int32_t ahead = find(step0 + 1);
         __syncthreads();  // left_out_any is cleared
         if (now) store(0, step0, now);
-        uint64_t next = __ballot(ahead >= 0);
-        if (next) load(ahead);
-        ahead = find(step0 + 2);
+        slots = row_slot(page, step0 + 1);
+        page = fetch(step0 + 2);
+        uint64_t next = __ballot(slots >= 0);
+        if (next) load(slots);
         __syncthreads();
         for (int32_t step = step0; step < step1; ++step) {
             const int buf = (step - step0) & 1;
             if (next) store(buf ^ 1, step + 1, next);
-            const uint64_t after = __ballot(ahead >= 0);
-            if (after) load(ahead);
-            ahead = find(step + 3);
-            if (now && mine > 0) {
-                if (R == 1 || mine == R) compute(std::integral_constant<int, R>(), buf, step, now);
-                else compute(std::integral_constant<int, R == 1 ? 1 : R - 1>(), buf, step, now);
-            }
+            slots = row_slot(page, step + 2);
+            page = fetch(step + 3);
+            const uint64_t after = __ballot(slots >= 0);
+            if (after) load(slots);
+            if (now && mine > 0) compute(buf, step, now);
             now = next;
             next = after;
             __syncthreads();
@@ -349,25 +381,39 @@ __global__ void __launch_bounds__(64 * NW, D == 256 && NW == 4 ? 1 : 2) wide_ker
             const int64_t t = u.tok + x / a.group;
             const int64_t o = t * a.heads * a.group + u.h * a.group + x % a.group;
             if (g == 0) {
+                const float top = row_top(m[r], to_log2);
                 if (!whole) {
-                    part[M * D + row] = m[r];
+                    part[M * D + row] = top;
                     part[M * D + M + row] = sum;
                 } else if (a.lse != nullptr) {
-                    a.lse[o] = some ? (m[r] + log2_fast(sum)) * kLn2 : -__builtin_inff();
+                    a.lse[o] = some ? (top + log2_fast(sum)) * kLn2 : -__builtin_inff();
                 }
             }
+            // Register i of tile n holds row 16 n + 4 g + i of V, so the tiles k, k + KT, .. hold CW
+            // consecutive channels.
+            constexpr int CW = PL::CW, KT = T::NT / CW;
 #pragma unroll
-            for (int n = 0; n < T::NT; ++n) {
-                const int d = n * 16 + g * 4;
-                float y[4];
+            for (int i = 0; i < 4; ++i)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) y[e] = acc[r][n][e] * inv;
-                if (left_out_any)
-                    add_left_out<BF16, MX, D>(a, q, u, t, (int64_t)step0 * kKeys,
-                                              (int64_t)step1 * kKeys, d, y);
-                if (whole) store_row<BF16, 4>(a.out, o * D + d, y);
-                else *reinterpret_cast<f32x4*>(part + row * D + d) = f32x4{y[0], y[1], y[2], y[3]};
-            }
+                for (int k = 0; k < KT; ++k) {
+                    const int d = (k * 16 + g * 4 + i) * CW;
+                    float y[CW];
+#pragma unroll
+                    for (int e = 0; e < CW; ++e) y[e] = acc[r][e * KT + k][i] * inv;
+                    if (whole) {
+                        store_row<BF16, CW>(a.out, o * D + d, y);
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < CW; e += 4)
+                            *reinterpret_cast<f32x4*>(part + row * D + d + e) =
+                                f32x4{y[e], y[e + 1], y[e + 2], y[e + 3]};
+                    }
+                }
+        }
+        if (left_out_any) {   // (set before the last step's barrier, the same for all)
+            __syncthreads();  // the rows are written
+            add_left_out<BF16, MX, D>(a, q, u, (int64_t)step0 * kKeys, (int64_t)step1 * kKeys,
+                                      whole ? nullptr : part);
         }
     }
 }
