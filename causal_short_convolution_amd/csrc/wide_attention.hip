@@ -18,7 +18,6 @@ namespace sc {
 namespace {
 
 constexpr int kKeys = 64;  // keys per step
-constexpr int kNoLds = 0x7f;  // scheduling barrier that everything but LDS accesses may cross
 
 template <int D>
 struct Places {
@@ -30,18 +29,26 @@ struct Places {
     __device__ static inline int v_row(int c, int e) { return e * (D / CW) + c; }
 };
 
-// What one thread loads of a step: pieces of K rows, and pieces of 4 rows of V.
-template <bool MX, int D, int NT>
+// What one thread loads of a step: pieces of 16 bytes of K rows, and the same CW channels of 4 rows
+// of V. Of 8 waves four load V and four load K, into the same registers; 4 waves load both.
+template <bool MX, int D, int NW>
 struct Pieces {
-    static constexpr int KP = MX ? D / 16 : D / 8;          // pieces of 16 bytes per K row
-    static constexpr int KN = (kKeys * KP + NT - 1) / NT;   // per thread
+    static constexpr bool SPLIT = NW == 8;
     static constexpr int CW = Places<D>::CW;
-    static constexpr int VP = D / CW;                       // pieces of CW channels per V row
-    static constexpr int VN = (kKeys / 4 * VP + NT - 1) / NT;
-    uint4 k[KN];
-    uint32_t v[VN][4][MX ? CW / 4 : CW / 2];
-    uint8_t ks[MX ? KN : 1];
-    uint8_t vs[MX ? VN : 1][4];
+    static constexpr int KP = MX ? D / 16 : D / 8;  // pieces per K row
+    static constexpr int KN = kKeys * KP / 256;     // pieces per thread
+    static constexpr int VP = D / CW;               // pieces per V row
+    static constexpr int VN = kKeys / 4 * VP / 256;
+    static constexpr int VW = MX ? CW / 4 : CW / 2; // words per piece of a V row
+    static constexpr int K_WORDS = KN * 4, V_WORDS = VN * 4 * VW;
+    static constexpr int V0 = SPLIT ? 0 : K_WORDS;
+    static constexpr int WORDS = !SPLIT ? K_WORDS + V_WORDS
+                                        : K_WORDS > V_WORDS ? K_WORDS : V_WORDS;
+    static constexpr int E0 = SPLIT ? 0 : KN;       // scale bytes: KN of K, 4 VN of V
+    static constexpr int SCALES = !MX ? 1 : !SPLIT ? KN + 4 * VN : KN > 4 * VN ? KN : 4 * VN;
+    static_assert(KN * 256 == kKeys * KP && VN * 256 == kKeys / 4 * VP, "whole shares");
+    uint32_t w[WORDS];
+    uint8_t e[SCALES];
 };
 
 template <bool MX, int D, int NW, int R>
@@ -52,7 +59,7 @@ __global__ void __launch_bounds__(64 * NW, D == 256 && NW == 4 ? 1 : 2) wide_ker
     constexpr int NT = 64 * NW;
     constexpr int M = 16 * R * NW;
     constexpr int WORKERS = wide_workers(NW, D);
-    using PC = Pieces<MX, D, NT>;
+    using PC = Pieces<MX, D, NW>;
     __shared__ __attribute__((aligned(16))) char kbuf[2][PL::K_BYTES];
     __shared__ __attribute__((aligned(16))) char vbuf[2][PL::V_BYTES];
     __shared__ RunScratch run;
@@ -109,10 +116,9 @@ __global__ void __launch_bounds__(64 * NW, D == 256 && NW == 4 ? 1 : 2) wide_ker
         // ---- a step's keys: lane l finds the row of key l (-1: there is none). The page id is
         // fetched a step before it is looked at, so that nothing waits for it.
         const int32_t* table = a.pg.table + (int64_t)u.s * a.pg.max_blocks;
-        const int32_t last = q.keys > 0 ? q.keys - 1 : 0;
         auto fetch = [&](int32_t step) -> int32_t {
             const int64_t p = (int64_t)step * kKeys + lane;
-            return q.keys > 0 ? table[(int32_t)min(p, (int64_t)last) >> a.pg.shift] : -1;
+            return table[(int32_t)min(p, (int64_t)q.keys - 1) >> a.pg.shift];
         };
         auto row_slot = [&](int32_t page, int32_t step) -> int32_t {
             const int64_t p = (int64_t)step * kKeys + lane;
@@ -120,98 +126,106 @@ __global__ void __launch_bounds__(64 * NW, D == 256 && NW == 4 ? 1 : 2) wide_ker
             return ok ? (page << a.pg.shift) + ((int32_t)p & ((1 << a.pg.shift) - 1)) : -1;
         };
         PC pc;
+        const int t8 = tid & 255;
+        // The n-th piece of V of this thread: keys 32 kb + 16 s + 4 gg .. + 3, channels CW ch ..
         auto v_item = [&](int n, int& kb, int& gg, int& s, int& ch) {
-            const int x = n * NT + tid;
+            const int x = n * 256 + t8;
             ch = x % PC::VP;
             const int y = x / PC::VP;
             s = y & 1;
             gg = (y >> 1) & 3;
             kb = y >> 3;
-            return kb < kKeys / 32;
         };
-        auto load = [&](int32_t slots) {
-            const int32_t row = slots < 0 ? 0 : slots;
+        // (a slot of -1 is loaded as row 0, which a pool with pages has)
+        auto load_k = [&](int32_t row) {
 #pragma unroll
             for (int n = 0; n < PC::KN; ++n) {
-                const int x = n * NT + tid;
-                const int key = x / PC::KP, p = x % PC::KP;
-                const int64_t r = (int64_t)__shfl(row, key & 63) * row_elems;
-                if (kKeys * PC::KP % NT == 0 || key < kKeys) {
-                    pc.k[n] = *reinterpret_cast<const uint4*>(kc + r * EB + p * 16);
-                    if constexpr (MX) pc.ks[n] = ks[r / 32 + p / 2];
-                }
+                const int x = n * 256 + t8;
+                const int64_t r = (int64_t)__shfl(row, x / PC::KP) * row_elems;
+                const u32x4 y = *reinterpret_cast<const u32x4*>(kc + r * EB + x % PC::KP * 16);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) pc.w[n * 4 + i] = y[i];
+                if constexpr (MX) pc.e[n] = ks[r / 32 + x % PC::KP / 2];
             }
+        };
+        auto load_v = [&](int32_t row) {
 #pragma unroll
             for (int n = 0; n < PC::VN; ++n) {
                 int kb, gg, s, ch;
-                const bool in = v_item(n, kb, gg, s, ch);
+                v_item(n, kb, gg, s, ch);
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
-                    const int key = (kb * 32 + s * 16 + gg * 4 + j) & 63;
-                    const int64_t r = (int64_t)__shfl(row, key) * row_elems;
-                    if (kKeys / 4 * PC::VP % NT == 0 || in) {
-                        const char* p = vc + r * EB + ch * PL::CW * EB;
-                        uint32_t(&w)[MX ? PL::CW / 4 : PL::CW / 2] = pc.v[n][j];
-                        if constexpr (PL::CW * EB == 16) {
-                            const uint4 x = *reinterpret_cast<const uint4*>(p);
-                            w[0] = x.x;
-                            w[1] = x.y;
-                            w[2] = x.z;
-                            w[3] = x.w;
-                        } else if constexpr (PL::CW * EB == 8) {
-                            const uint2 x = *reinterpret_cast<const uint2*>(p);
-                            w[0] = x.x;
-                            w[1] = x.y;
-                        } else {
-                            w[0] = *reinterpret_cast<const uint32_t*>(p);
-                        }
-                        if constexpr (MX) pc.vs[n][j] = vs[r / 32 + ch * PL::CW / 32];
+                    const int64_t r =
+                        (int64_t)__shfl(row, kb * 32 + s * 16 + gg * 4 + j) * row_elems;
+                    const char* p = vc + r * EB + ch * PL::CW * EB;
+                    uint32_t* w = pc.w + PC::V0 + (n * 4 + j) * PC::VW;
+                    if constexpr (PC::VW == 4) {
+                        const u32x4 y = *reinterpret_cast<const u32x4*>(p);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) w[i] = y[i];
+                    } else if constexpr (PC::VW == 2) {
+                        const u32x2_t y = *reinterpret_cast<const u32x2_t*>(p);
+                        w[0] = y[0];
+                        w[1] = y[1];
+                    } else {
+                        w[0] = *reinterpret_cast<const uint32_t*>(p);
                     }
+                    if constexpr (MX) pc.e[PC::E0 + n * 4 + j] = vs[r / 32 + ch * PL::CW / 32];
                 }
             }
         };
-        auto store = [&](int buf, int32_t step, uint64_t valid) {
+        auto load = [&](int32_t slots) {
+            const int32_t row = slots < 0 ? 0 : slots;
+            if constexpr (PC::SPLIT) {
+                if (wave < 4) load_v(row);
+                else load_k(row);
+            } else {
+                load_k(row);
+                load_v(row);
+            }
+        };
+        auto store_k = [&](int buf) {
 #pragma unroll
             for (int n = 0; n < PC::KN; ++n) {
-                const int x = n * NT + tid;
-                const int key = x / PC::KP, p = x % PC::KP;
-                if (kKeys * PC::KP % NT == 0 || key < kKeys) {
-                    char* to = kbuf[buf] + key * PL::KROW;
-                    if constexpr (MX) {
-                        const float e = e8m0(pc.ks[n]);
-                        const uint32_t w[4] = {pc.k[n].x, pc.k[n].y, pc.k[n].z, pc.k[n].w};
+                const int x = n * 256 + t8;
+                char* to = kbuf[buf] + x / PC::KP * PL::KROW + x % PC::KP * (MX ? 32 : 16);
+                const uint32_t* w = pc.w + n * 4;
+                if constexpr (MX) {
+                    const float e = e8m0(pc.e[n]);
 #pragma unroll
-                        for (int i = 0; i < 2; ++i)
-                            *reinterpret_cast<uint4*>(to + p * 32 + i * 16) = make_uint4(
-                                X::widen2(w[2 * i], e, false), X::widen2(w[2 * i], e, true),
-                                X::widen2(w[2 * i + 1], e, false), X::widen2(w[2 * i + 1], e, true));
-                    } else {
-                        *reinterpret_cast<uint4*>(to + p * 16) = pc.k[n];
-                    }
+                    for (int i = 0; i < 2; ++i)
+                        *reinterpret_cast<u32x4*>(to + i * 16) = u32x4{
+                            X::widen2(w[2 * i], e, false), X::widen2(w[2 * i], e, true),
+                            X::widen2(w[2 * i + 1], e, false), X::widen2(w[2 * i + 1], e, true)};
+                } else {
+                    *reinterpret_cast<u32x4*>(to) = u32x4{w[0], w[1], w[2], w[3]};
                 }
             }
+        };
+        auto store_v = [&](int buf, int32_t step, uint64_t valid) {
             const bool plain = valid == ~0ull && (int64_t)(step + 1) * kKeys <= q.ctx;
 #pragma unroll
             for (int n = 0; n < PC::VN; ++n) {
                 int kb, gg, s, ch;
-                const bool in = v_item(n, kb, gg, s, ch);
-                if (!(kKeys / 4 * PC::VP % NT == 0 || in)) continue;
+                v_item(n, kb, gg, s, ch);
                 constexpr int CP = PL::CW / 2;
                 uint32_t w[4][CP];  // [key][channel pair]
 #pragma unroll
                 for (int j = 0; j < 4; ++j)
 #pragma unroll
                     for (int i = 0; i < CP; ++i) {
+                        const uint32_t* from = pc.w + PC::V0 + (n * 4 + j) * PC::VW;
                         if constexpr (MX)
-                            w[j][i] = X::widen2(pc.v[n][j][i / 2], e8m0(pc.vs[n][j]), i & 1);
+                            w[j][i] =
+                                X::widen2(from[i / 2], e8m0(pc.e[PC::E0 + n * 4 + j]), i & 1);
                         else
-                            w[j][i] = pc.v[n][j][i];
+                            w[j][i] = from[i];
                     }
                 if (!plain) {
-                    // Keys that do not exist count as zeros. Among the new tokens a row of V may be
-                    // one that only some query rows look at, and an infinity or a NaN times a weight
-                    // of zero would reach the others: those elements are left out here and added
-                    // at the end of the unit to the rows that do look at them.
+                    // Keys that do not exist count as zeros. Among the new tokens a row of V may
+                    // be one that only some query rows look at, and an infinity or a NaN times
+                    // a weight of zero would reach the others: those elements are left out here
+                    // and added at the end of the unit to the rows that do look at them.
                     bool any = false;
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
@@ -230,13 +244,22 @@ __global__ void __launch_bounds__(64 * NW, D == 256 && NW == 4 ? 1 : 2) wide_ker
 #pragma unroll
                 for (int e = 0; e < PL::CW; ++e) {
                     const uint32_t sel = (e & 1) ? 0x07060302u : 0x05040100u;
-                    const uint2 pair = make_uint2(
+                    const u32x2_t pair = {
                         __builtin_amdgcn_perm(w[1][e / 2], w[0][e / 2], sel),
-                        __builtin_amdgcn_perm(w[3][e / 2], w[2][e / 2], sel));
+                        __builtin_amdgcn_perm(w[3][e / 2], w[2][e / 2], sel)};
                     // keys i, i + 16 for i = 32 kb + 4 g .. share a group of 16 bytes
-                    *reinterpret_cast<uint2*>(vbuf[buf] + PL::v_row(ch, e) * PL::VROW +
-                                              (kb * 4 + gg) * 16 + s * 8) = pair;
+                    *reinterpret_cast<u32x2_t*>(vbuf[buf] + PL::v_row(ch, e) * PL::VROW +
+                                                (kb * 4 + gg) * 16 + s * 8) = pair;
                 }
+            }
+        };
+        auto store = [&](int buf, int32_t step, uint64_t valid) {
+            if constexpr (PC::SPLIT) {
+                if (wave < 4) store_v(buf, step, valid);
+                else store_k(buf);
+            } else {
+                store_k(buf);
+                store_v(buf, step, valid);
             }
         };
 
@@ -250,7 +273,7 @@ __global__ void __launch_bounds__(64 * NW, D == 256 && NW == 4 ? 1 : 2) wide_ker
             for (int i = 0; i < T::NT; ++i) acc[r][i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
         }
         // One step for the wave's row tiles. LDS is read AHEAD operands ahead of
-        // the products that take them (the barriers keep LDS reads where they are written).
+        // the products that take them (the scheduling barriers keep them so).
         auto compute = [&](int buf, int32_t step, uint64_t valid) {
             const int32_t k0 = step * kKeys;
             const char* kb = kbuf[buf] + c * PL::KROW + g * 16;
@@ -274,6 +297,7 @@ __global__ void __launch_bounds__(64 * NW, D == 256 && NW == 4 ? 1 : 2) wide_ker
                 for (int s = 0; s < 4; ++s) x[r][s] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
             for (int i = 0; i < AHEAD; ++i) read_k(i);
+            __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
             for (int i = 0; i < NK; ++i) {
 #pragma unroll
@@ -281,7 +305,7 @@ __global__ void __launch_bounds__(64 * NW, D == 256 && NW == 4 ? 1 : 2) wide_ker
                     x[r][i / T::NF] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
                         op[i % AHEAD], qreg[r][i % T::NF], x[r][i / T::NF], 0, 0, 0);
                 if (i + AHEAD < NK) read_k(i + AHEAD);
-                __builtin_amdgcn_sched_barrier(kNoLds);
+                __builtin_amdgcn_sched_barrier(0);
             }
             if (valid != ~0ull || k0 + kKeys > q.ctx) {  // some rows do not look at some keys
 #pragma unroll
@@ -299,7 +323,7 @@ __global__ void __launch_bounds__(64 * NW, D == 256 && NW == 4 ? 1 : 2) wide_ker
             }
 #pragma unroll
             for (int i = 0; i < AHEAD; ++i) read_v(i);
-            __builtin_amdgcn_sched_barrier(kNoLds);
+            __builtin_amdgcn_sched_barrier(0);
             bf16x8 p[R][2];
 #pragma unroll
             for (int r = 0; r < R; ++r) {
@@ -338,33 +362,38 @@ __global__ void __launch_bounds__(64 * NW, D == 256 && NW == 4 ? 1 : 2) wide_ker
                     acc[r][i / 2] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
                         op[i % AHEAD], p[r][i % 2], acc[r][i / 2], 0, 0, 0);
                 if (i + AHEAD < NV) read_v(i + AHEAD);
-                __builtin_amdgcn_sched_barrier(kNoLds);
+                __builtin_amdgcn_sched_barrier(0);
             }
         };
         __syncthreads();  // the last unit is done with LDS
         if (tid == 0) left_out_any = 0;
-        int32_t slots = row_slot(fetch(step0), step0);
-        int32_t page = fetch(step0 + 1);
-        uint64_t now = __ballot(slots >= 0);
-        if (now) load(slots);
-        __syncthreads();  // left_out_any is cleared
-        if (now) store(0, step0, now);
-        slots = row_slot(page, step0 + 1);
-        page = fetch(step0 + 2);
-        uint64_t next = __ballot(slots >= 0);
-        if (next) load(slots);
-        __syncthreads();
-        for (int32_t step = step0; step < step1; ++step) {
-            const int buf = (step - step0) & 1;
-            if (next) store(buf ^ 1, step + 1, next);
-            slots = row_slot(page, step + 2);
-            page = fetch(step + 3);
-            const uint64_t after = __ballot(slots >= 0);
-            if (after) load(slots);
-            if (now && mine > 0) compute(buf, step, now);
-            now = next;
-            next = after;
+        if (q.keys > 0 && a.pg.num_pages > 0) {
+            // (steps past the last are loaded as row 0 and count as no keys)
+            int32_t slots = row_slot(fetch(step0), step0);
+            int32_t page = fetch(step0 + 1);
+            uint64_t now = __ballot(slots >= 0);
+            load(slots);
+            __syncthreads();  // left_out_any is cleared
+            store(0, step0, now);
+            slots = row_slot(page, step0 + 1);
+            page = fetch(step0 + 2);
+            uint64_t next = __ballot(slots >= 0);
+            load(slots);
             __syncthreads();
+            for (int32_t step = step0; step < step1; ++step) {
+                const int buf = (step - step0) & 1;
+                store(buf ^ 1, step + 1, next);
+                slots = row_slot(page, step + 2);
+                page = fetch(step + 3);
+                const uint64_t after = __ballot(slots >= 0);
+                load(slots);
+                if (now && mine > 0) compute(buf, step, now);
+                now = next;
+                next = after;
+                __syncthreads();
+            }
+        } else {
+            __syncthreads();  // left_out_any is cleared
         }
 
         // ---- every wave writes its own rows
