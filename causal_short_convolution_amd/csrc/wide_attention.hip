@@ -9,9 +9,10 @@
 // step t is computed from one, step t + 1, loaded to registers a step earlier, is written to the
 // other, and the loads of step t + 2 are under way. One barrier per step.
 //
-// LDS rows are padded by 16 bytes, and the row of channel CW c + e of V (CW = 8, for heads of 64 4) is
-// e D / CW + c, so that the lanes that an LDS access serves at a time fall on different banks both
-// where CW channels of 4 keys are written and where 16 rows of 8 keys are read.
+// Rows in LDS are not padded; their 16-byte pieces are permuted by exclusive or with bits of the row,
+// so that the lanes that an access serves at a time fall on different banks: 16 rows of one piece
+// (or of two neighbouring pieces, rows 4 by 4) where operands are read, whole rows and 16 rows of V
+// where they are written. Padding rows by 16 bytes instead cost 850 conflict cycles of 5000 per step.
 #include "attention_line.h"
 
 namespace sc {
@@ -21,12 +22,27 @@ constexpr int kKeys = 64;  // keys per step
 
 template <int D>
 struct Places {
-    static constexpr int KROW = D * 2 + 16;
-    static constexpr int VROW = kKeys * 2 + 16;
+    static constexpr int KROW = D * 2;
+    static constexpr int VROW = kKeys * 2;
     static constexpr int K_BYTES = kKeys * KROW;
     static constexpr int V_BYTES = D * VROW;
+    // What the piece numbers of a row of BYTES are permuted by: 256 bytes hold all banks, so rows of
+    // 128 change it every second row.
+    template <int BYTES>
+    __device__ static inline int turn(int row) {
+        return BYTES == 128 ? (row >> 1) & 7 : row & 15;
+    }
+    // Place of 16-byte piece `piece` of the K row of key `key`.
+    __device__ static inline int k(int key, int piece) {
+        return key * KROW + ((piece ^ turn<KROW>(key)) << 4);
+    }
+    // V's rows: channel CW c + e is row e D / CW + c, which holds the keys i, i + 16 for
+    // i = 32 kb + 4 g .. (in the order of the weights) as its piece 4 kb + g.
     static constexpr int CW = D / 16 < 8 ? D / 16 : 8;  // channels that a thread turns at a time
     __device__ static inline int v_row(int c, int e) { return e * (D / CW) + c; }
+    __device__ static inline int v(int row, int piece) {
+        return row * VROW + ((piece ^ turn<VROW>(row)) << 4);
+    }
 };
 
 // What one thread loads of a step: pieces of 16 bytes of K rows, and the same CW channels of 4 rows
@@ -69,7 +85,7 @@ __global__ void __launch_bounds__(64 * NW, D == 256 && NW == 4 ? 1 : 2) wide_ker
     const int wave = uniform(tid >> 6);
     const int c = lane & 15, g = lane >> 4;
     constexpr int EB = MX ? 1 : 2;
-    const int64_t row_elems = (int64_t)a.heads * D;
+    const uint32_t row_bytes = (uint32_t)(a.heads * D * EB);
     char* ws = static_cast<char*>(a.ws);
 
     const int64_t total = find_run<kKeys, M, WORKERS, NT>(a, reinterpret_cast<int64_t*>(ws), run);
@@ -117,13 +133,14 @@ __global__ void __launch_bounds__(64 * NW, D == 256 && NW == 4 ? 1 : 2) wide_ker
         // fetched a step before it is looked at, so that nothing waits for it.
         const int32_t* table = a.pg.table + (int64_t)u.s * a.pg.max_blocks;
         auto fetch = [&](int32_t step) -> int32_t {
-            const int64_t p = (int64_t)step * kKeys + lane;
-            return table[(int32_t)min(p, (int64_t)q.keys - 1) >> a.pg.shift];
+            const uint32_t p = (uint32_t)step * kKeys + lane;
+            return table[min(p, (uint32_t)q.keys - 1) >> a.pg.shift];
         };
         auto row_slot = [&](int32_t page, int32_t step) -> int32_t {
-            const int64_t p = (int64_t)step * kKeys + lane;
-            const bool ok = step < step1 && p < q.keys && page >= 0 && page < a.pg.num_pages;
-            return ok ? (page << a.pg.shift) + ((int32_t)p & ((1 << a.pg.shift) - 1)) : -1;
+            const uint32_t p = (uint32_t)step * kKeys + lane;
+            const bool ok = step < step1 && p < (uint32_t)q.keys && page >= 0 &&
+                            page < a.pg.num_pages;
+            return ok ? (page << a.pg.shift) + (int32_t)(p & ((1u << a.pg.shift) - 1u)) : -1;
         };
         PC pc;
         const int t8 = tid & 255;
@@ -136,13 +153,20 @@ __global__ void __launch_bounds__(64 * NW, D == 256 && NW == 4 ? 1 : 2) wide_ker
             gg = (y >> 1) & 3;
             kb = y >> 3;
         };
-        // (a slot of -1 is loaded as row 0, which a pool with pages has)
+        // With pages of at least a step's keys the step's rows lie one after the other behind a row
+        // that is the same for all lanes, and only scalars change from step to step.
+        const bool one_page = (1 << a.pg.shift) >= kKeys;
+        auto row_of_key = [&](int32_t row, int key) -> int64_t {  // in bytes
+            return one_page ? uniform((int64_t)((uint64_t)(uint32_t)uniform(row) * row_bytes)) +
+                                  (uint32_t)key * row_bytes
+                            : (int64_t)((uint64_t)(uint32_t)__shfl(row, key) * row_bytes);
+        };
         auto load_k = [&](int32_t row) {
 #pragma unroll
             for (int n = 0; n < PC::KN; ++n) {
                 const int x = n * 256 + t8;
-                const int64_t r = (int64_t)__shfl(row, x / PC::KP) * row_elems;
-                const u32x4 y = *reinterpret_cast<const u32x4*>(kc + r * EB + x % PC::KP * 16);
+                const int64_t r = row_of_key(row, x / PC::KP);
+                const u32x4 y = *reinterpret_cast<const u32x4*>(kc + r + x % PC::KP * 16);
 #pragma unroll
                 for (int i = 0; i < 4; ++i) pc.w[n * 4 + i] = y[i];
                 if constexpr (MX) pc.e[n] = ks[r / 32 + x % PC::KP / 2];
@@ -155,9 +179,8 @@ __global__ void __launch_bounds__(64 * NW, D == 256 && NW == 4 ? 1 : 2) wide_ker
                 v_item(n, kb, gg, s, ch);
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
-                    const int64_t r =
-                        (int64_t)__shfl(row, kb * 32 + s * 16 + gg * 4 + j) * row_elems;
-                    const char* p = vc + r * EB + ch * PL::CW * EB;
+                    const int64_t r = row_of_key(row, kb * 32 + s * 16 + gg * 4 + j);
+                    const char* p = vc + r + ch * PL::CW * EB;
                     uint32_t* w = pc.w + PC::V0 + (n * 4 + j) * PC::VW;
                     if constexpr (PC::VW == 4) {
                         const u32x4 y = *reinterpret_cast<const u32x4*>(p);
@@ -174,6 +197,7 @@ __global__ void __launch_bounds__(64 * NW, D == 256 && NW == 4 ? 1 : 2) wide_ker
                 }
             }
         };
+        // (a slot of -1 is loaded as row 0, which a pool with pages has)
         auto load = [&](int32_t slots) {
             const int32_t row = slots < 0 ? 0 : slots;
             if constexpr (PC::SPLIT) {
@@ -188,17 +212,18 @@ __global__ void __launch_bounds__(64 * NW, D == 256 && NW == 4 ? 1 : 2) wide_ker
 #pragma unroll
             for (int n = 0; n < PC::KN; ++n) {
                 const int x = n * 256 + t8;
-                char* to = kbuf[buf] + x / PC::KP * PL::KROW + x % PC::KP * (MX ? 32 : 16);
+                const int key = x / PC::KP, piece = x % PC::KP;
                 const uint32_t* w = pc.w + n * 4;
                 if constexpr (MX) {
                     const float e = e8m0(pc.e[n]);
 #pragma unroll
                     for (int i = 0; i < 2; ++i)
-                        *reinterpret_cast<u32x4*>(to + i * 16) = u32x4{
+                        *reinterpret_cast<u32x4*>(kbuf[buf] + PL::k(key, piece * 2 + i)) = u32x4{
                             X::widen2(w[2 * i], e, false), X::widen2(w[2 * i], e, true),
                             X::widen2(w[2 * i + 1], e, false), X::widen2(w[2 * i + 1], e, true)};
                 } else {
-                    *reinterpret_cast<u32x4*>(to) = u32x4{w[0], w[1], w[2], w[3]};
+                    *reinterpret_cast<u32x4*>(kbuf[buf] + PL::k(key, piece)) =
+                        u32x4{w[0], w[1], w[2], w[3]};
                 }
             }
         };
@@ -247,9 +272,8 @@ __global__ void __launch_bounds__(64 * NW, D == 256 && NW == 4 ? 1 : 2) wide_ker
                     const u32x2_t pair = {
                         __builtin_amdgcn_perm(w[1][e / 2], w[0][e / 2], sel),
                         __builtin_amdgcn_perm(w[3][e / 2], w[2][e / 2], sel)};
-                    // keys i, i + 16 for i = 32 kb + 4 g .. share a group of 16 bytes
-                    *reinterpret_cast<u32x2_t*>(vbuf[buf] + PL::v_row(ch, e) * PL::VROW +
-                                                (kb * 4 + gg) * 16 + s * 8) = pair;
+                    *reinterpret_cast<u32x2_t*>(
+                        vbuf[buf] + PL::v(PL::v_row(ch, e), kb * 4 + gg) + s * 8) = pair;
                 }
             }
         };
@@ -276,19 +300,17 @@ __global__ void __launch_bounds__(64 * NW, D == 256 && NW == 4 ? 1 : 2) wide_ker
         // the products that take them (the scheduling barriers keep them so).
         auto compute = [&](int buf, int32_t step, uint64_t valid) {
             const int32_t k0 = step * kKeys;
-            const char* kb = kbuf[buf] + c * PL::KROW + g * 16;
-            const char* vb = vbuf[buf] + c * PL::VROW + g * 16;
             // operand i of K: subtile i / NF, channels f = i % NF; of V: channel tile i / 2, keys 32 (i % 2)
             constexpr int AHEAD = 4;
             constexpr int NK = 4 * T::NF, NV = 2 * T::NT;
             bf16x8 op[AHEAD];
             auto read_k = [&](int i) {
-                op[i % AHEAD] = *reinterpret_cast<const bf16x8*>(kb + i / T::NF * 16 * PL::KROW +
-                                                                 i % T::NF * 64);
+                op[i % AHEAD] = *reinterpret_cast<const bf16x8*>(
+                    kbuf[buf] + i / T::NF * 16 * PL::KROW + PL::k(c, i % T::NF * 4 + g));
             };
             auto read_v = [&](int i) {
-                op[i % AHEAD] = *reinterpret_cast<const bf16x8*>(vb + i / 2 * 16 * PL::VROW +
-                                                                 i % 2 * 64);
+                op[i % AHEAD] = *reinterpret_cast<const bf16x8*>(
+                    vbuf[buf] + i / 2 * 16 * PL::VROW + PL::v(c, i % 2 * 4 + g));
             };
             f32x4 x[R][4];
 #pragma unroll
