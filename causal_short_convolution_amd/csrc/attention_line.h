@@ -8,28 +8,30 @@
 
 namespace sc {
 
-// `total` steps over WORKERS workers: worker w owns [begin(w), begin(w + 1)).
+// A line of `total` units of cost over at most WORKERS workers, each with no less than `most`, the
+// cost of one step: worker w owns the steps that start in [begin(w), begin(w + 1)).
 template <int WORKERS>
 struct Shares {
     int64_t total, each, more;
     int32_t workers;
-    __device__ Shares(int64_t t) : total(t) {
-        workers = (int32_t)(t < WORKERS ? t : WORKERS);
+    __device__ Shares(int64_t t, int32_t most) : total(t) {
+        const int64_t n = t / most;
+        workers = (int32_t)(n < WORKERS ? n : WORKERS);
         each = workers ? t / workers : 0;
         more = workers ? t - each * workers : 0;
     }
     __device__ int64_t begin(int32_t w) const { return w * each + (w < more ? w : more); }
-    __device__ int32_t owner(int64_t step) const {
+    __device__ int32_t owner(int64_t at) const {
         const int64_t cut = more * (each + 1);
-        return (int32_t)(step < cut ? step / (each + 1) : more + (step - cut) / each);
+        return (int32_t)(at < cut ? at / (each + 1) : more + (at - cut) / each);
     }
     // The worker that this workgroup is. Workgroups go round the 8 XCDs by blockIdx. Where every
-    // worker has steps, consecutive runs go to one XCD, so that units that read the same rows
-    // meet in its L2; fewer steps than workers are spread over the XCDs.
+    // workgroup has work, consecutive runs go to one XCD, so that units that read the same rows
+    // meet in its L2; fewer are spread over the XCDs.
     __device__ int32_t me() const {
-        return total < WORKERS ? (int32_t)blockIdx.x
-                               : (int32_t)(blockIdx.x & 7) * (WORKERS / 8) +
-                                     (int32_t)(blockIdx.x >> 3);
+        return workers < WORKERS ? (int32_t)blockIdx.x
+                                 : (int32_t)(blockIdx.x & 7) * (WORKERS / 8) +
+                                       (int32_t)(blockIdx.x >> 3);
     }
 };
 
@@ -41,27 +43,55 @@ struct Unit {
     int32_t row0;       // first query row (of the sequence's len * group, or the token's group)
     int32_t rows;       // rows in this unit, 1 .. M
     int32_t steps;      // steps of all its keys, at least 1
-    int64_t tok;        // selected pages: the token
-    int64_t first;      // its first step in the line
+    int32_t cost;       // of one step
+    int64_t tok;        // selected pages: the token; else the sequence's first
+    int64_t first;      // its place in the line
+    // The first step at or behind place `at` of the line, at most `steps`.
+    __device__ int32_t step_at(int64_t at) const {
+        const int64_t n = at <= first ? 0 : (at - first + cost - 1) / cost;
+        return (int32_t)(n < steps ? n : steps);
+    }
+    __device__ int64_t end() const { return first + (int64_t)steps * cost; }
 };
 
-// Sizes in steps of KS keys and units of M rows.
-template <int KS, int M>
+// Sizes in steps of KS keys and units of M rows. A step costs what loading its keys does, LOAD, and
+// one for each tile of 16 rows; where LOAD is 0, every wave does all rows of a step, filled or not,
+// and each step counts 1.
+template <int KS_, int M_, int LOAD_>
 struct Steps {
+    static constexpr int KS = KS_, M = M_, LOAD = LOAD_;
+    __device__ static inline int32_t cost(int32_t rows) {
+        return LOAD == 0 ? 1 : LOAD + (rows + 15) / 16;
+    }
+    static constexpr int32_t kMost = LOAD == 0 ? 1 : LOAD + M / 16;
     __device__ static inline int64_t of_keys(int64_t keys) {
         return keys > KS ? (keys + KS - 1) / KS : 1;
     }
-    // Steps of a sequence: its cache heads, times its row tiles, times its key steps.
+    // Cost of a step of all units of one head, the whole ones and the last.
+    __device__ static inline int64_t of_rows(int64_t rows) {
+        const int64_t whole = rows / M;
+        const int32_t rest = (int32_t)(rows - whole * M);
+        return whole * kMost + (rest ? cost(rest) : 0);
+    }
+    // Cost of a sequence: its cache heads, times the units of its rows, times its key steps.
     __device__ static inline int64_t of_sequence(const AttnArgs& a, const SeqInfo& q) {
         if (q.len == 0) return 0;
-        const int64_t tiles = ((int64_t)q.len * a.group + M - 1) / M;
-        return a.heads * tiles * of_keys(q.keys);
+        return a.heads * of_rows((int64_t)q.len * a.group) * of_keys(q.keys);
     }
     __device__ static inline int32_t of_pages(const AttnArgs& a) {
         return (int32_t)of_keys((int64_t)a.topk << a.pg.shift);
     }
     __device__ static inline int32_t group_tiles(const AttnArgs& a) {
         return (a.group + M - 1) / M;
+    }
+    // The unit of row `row` (of the sequence's, or the token's) of head h, behind `head0`, where
+    // the line's units of its head begin.
+    __device__ static inline void place(Unit& u, int64_t rows, int64_t row, int64_t head0) {
+        const int64_t index = row / M;
+        u.row0 = (int32_t)(index * M);
+        u.rows = (int32_t)(rows - u.row0 < M ? rows - u.row0 : M);
+        u.cost = cost(u.rows);
+        u.first = head0 + index * u.steps * kMost;
     }
 };
 
@@ -72,17 +102,17 @@ struct RunScratch {
     int32_t s;
 };
 
-// By the whole workgroup: the number of steps of all sequences; in `scratch` the sequence that this
-// worker's first step lies in and that sequence's first step. The first worker leaves the prefix
-// sums for the joining launch in `prefix`.
-template <int KS, int M, int WORKERS, int THREADS>
+// By the whole workgroup: the cost of all sequences; in `scratch` the sequence that this worker's run
+// begins in and that sequence's place in the line. The first worker leaves the prefix sums for the
+// joining launch in `prefix`.
+template <class S, int WORKERS, int THREADS>
 __device__ inline int64_t find_run(const AttnArgs& a, int64_t* prefix, RunScratch& scratch) {
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     const int per = (a.b.num_seqs + THREADS - 1) / THREADS;
     int64_t mine = 0;
     for (int j = 0; j < per; ++j) {
         const int s = tid * per + j;
-        if (s < a.b.num_seqs) mine += Steps<KS, M>::of_sequence(a, seq_info(a.b, a.pg, s));
+        if (s < a.b.num_seqs) mine += S::of_sequence(a, seq_info(a.b, a.pg, s));
     }
     int64_t inc = mine;
     for (int d = 1; d < 64; d <<= 1) {
@@ -96,14 +126,14 @@ __device__ inline int64_t find_run(const AttnArgs& a, int64_t* prefix, RunScratc
         if (w < wave) before += scratch.sums[w];
         total += scratch.sums[w];
     }
-    const Shares<WORKERS> sh(total);
+    const Shares<WORKERS> sh(total, S::kMost);
     const int32_t me = sh.me();
     const int64_t want = me < sh.workers ? sh.begin(me) : -1;
     int64_t x = before + inc - mine;
     for (int j = 0; j < per; ++j) {
         const int s = tid * per + j;
         if (s >= a.b.num_seqs) break;
-        const int64_t n = Steps<KS, M>::of_sequence(a, seq_info(a.b, a.pg, s));
+        const int64_t n = S::of_sequence(a, seq_info(a.b, a.pg, s));
         if (want >= x && want < x + n) {
             scratch.s = s;
             scratch.first = x;
@@ -116,27 +146,25 @@ __device__ inline int64_t find_run(const AttnArgs& a, int64_t* prefix, RunScratc
     return total;
 }
 
-// The unit of step `at` in a line of whole sequences; u.s, q and seq_first (the first step of
-// sequence u.s) move on as needed.
-template <int KS, int M>
-__device__ inline void unit_of_step(const AttnArgs& a, int64_t at, Unit& u, SeqInfo& q,
-                                    int64_t& seq_first) {
-    int64_t n = Steps<KS, M>::of_sequence(a, q);
+// The unit of place `at` in a line of whole sequences; u.s, q and seq_first (where sequence u.s
+// begins) move on as needed.
+template <class S>
+__device__ inline void unit_at(const AttnArgs& a, int64_t at, Unit& u, SeqInfo& q,
+                               int64_t& seq_first) {
+    int64_t n = S::of_sequence(a, q);
     while (at >= seq_first + n) {
         seq_first += n;
         q = seq_info(a.b, a.pg, ++u.s);
-        n = Steps<KS, M>::of_sequence(a, q);
+        n = S::of_sequence(a, q);
     }
-    u.steps = (int32_t)Steps<KS, M>::of_keys(q.keys);
-    const int64_t rows = (int64_t)q.len * a.group;
-    const int64_t tiles = (rows + M - 1) / M;
-    const int64_t index = (at - seq_first) / u.steps;
-    u.first = seq_first + index * u.steps;
-    u.h = (int32_t)(index / tiles);
-    const int64_t r0 = index % tiles * M;
-    u.row0 = (int32_t)r0;
-    u.rows = (int32_t)(rows - r0 < M ? rows - r0 : M);
+    u.steps = (int32_t)S::of_keys(q.keys);
     u.tok = q.start;
+    const int64_t rows = (int64_t)q.len * a.group;
+    const int64_t head = S::of_rows(rows) * u.steps;  // cost of one head
+    u.h = (int32_t)((at - seq_first) / head);
+    const int64_t head0 = seq_first + u.h * head;
+    const int64_t whole = (int64_t)u.steps * S::kMost;
+    S::place(u, rows, (at - head0) / whole * S::M, head0);
 }
 
 // A part of a unit that worker `me` computed, in the workspace: M rows of D sums, then the rows'
@@ -181,9 +209,9 @@ __device__ inline void add_left_out(const AttnArgs& a, const SeqInfo& q, const U
 }
 
 // Joins the parts of the units that crossed workers: one wave per (token, query head).
-template <class E, int D, int KS, int M, int WORKERS, bool SPARSE>
+template <class E, int D, class S, int WORKERS, bool SPARSE>
 __global__ void __launch_bounds__(256) join_kernel(AttnArgs a) {
-    using S = Steps<KS, M>;
+    constexpr int M = S::M;
     constexpr int N = D / 64;
     const int lane = threadIdx.x & 63;
     const int64_t t = blockIdx.x;
@@ -195,25 +223,26 @@ __global__ void __launch_bounds__(256) join_kernel(AttnArgs a) {
     if (i < 0 || i >= q.len) return;
     const char* ws = static_cast<const char*>(a.ws);
     const int h = hq / a.group;
-    int64_t first, total;
-    int32_t steps, row;
+    int64_t total;
+    int32_t row;
+    Unit u;
     if constexpr (SPARSE) {
-        steps = S::of_pages(a);
+        u.steps = S::of_pages(a);
         const int32_t tiles = S::group_tiles(a);
         row = hq - h * a.group;
-        first = ((t * a.heads + h) * tiles + row / M) * steps;
-        total = a.b.tokens * a.heads * tiles * steps;
+        S::place(u, a.group, row, (t * a.heads + h) * tiles * u.steps);
+        total = a.b.tokens * a.heads * tiles * u.steps;
     } else {
         const int64_t* prefix = reinterpret_cast<const int64_t*>(ws);
-        steps = (int32_t)S::of_keys(q.keys);
-        const int64_t tiles = ((int64_t)q.len * a.group + M - 1) / M;
+        u.steps = (int32_t)S::of_keys(q.keys);
+        const int64_t rows = (int64_t)q.len * a.group;
         row = (int32_t)(i * a.group + hq - h * a.group);
-        first = prefix[s] + (h * tiles + row / M) * steps;
+        S::place(u, rows, row, prefix[s] + h * S::of_rows(rows) * u.steps);
         total = prefix[a.b.num_seqs];
     }
-    row %= M;
-    const Shares<WORKERS> sh(total);
-    const int32_t w0 = sh.owner(first), w1 = sh.owner(first + steps - 1);
+    row -= u.row0;
+    const Shares<WORKERS> sh(total, S::kMost);
+    const int32_t w0 = sh.owner(u.first), w1 = sh.owner(u.end() - u.cost);
     if (w0 == w1) return;  // written by its worker
     auto part = [&](int32_t w) { return part_of<M, D>(a.ws, a.part_offset, w, w == w0); };
     // lane i takes the maximum and the sum of part w0 + i, 64 parts at a time
@@ -263,10 +292,10 @@ __global__ void __launch_bounds__(256) join_kernel(AttnArgs a) {
         a.lse[at] = some ? (big + log2_fast(sum)) * kLn2 : -__builtin_inff();
 }
 
-template <class E, int D, int KS, int M, int WORKERS, bool SPARSE>
+template <class E, int D, class S, int WORKERS, bool SPARSE>
 hipError_t launch_join(const AttnArgs& a, hipStream_t st) {
     const dim3 grid((uint32_t)a.b.tokens, (uint32_t)(a.heads * a.group + 3) / 4);
-    join_kernel<E, D, KS, M, WORKERS, SPARSE><<<grid, 256, 0, st>>>(a);
+    join_kernel<E, D, S, WORKERS, SPARSE><<<grid, 256, 0, st>>>(a);
     return hipGetLastError();
 }
 

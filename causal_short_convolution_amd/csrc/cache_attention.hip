@@ -27,6 +27,7 @@ __global__ void __launch_bounds__(kBlock, 2) attention_kernel(AttnArgs a) {
     constexpr int SUB = T::SUB;
     constexpr int KW = 16 * SUB;      // keys per wave and step
     constexpr int KS = KW * kWaves;   // keys per step
+    using S = Steps<KS, M, 0>;
     constexpr uint32_t kFull = SUB == 2 ? 0xffffffffu : 0xffffu;
     constexpr int QSTRIDE = D * T::QB + 16;  // query rows in LDS, staggered over the banks
     constexpr bool QREG = R == 1 && D <= 128;  // query operands stay in registers
@@ -49,12 +50,12 @@ __global__ void __launch_bounds__(kBlock, 2) attention_kernel(AttnArgs a) {
     int64_t total, at, end;
     Unit u;
     if constexpr (SPARSE) {
-        u.steps = Steps<KS, M>::of_pages(a);
-        total = a.b.tokens * a.heads * Steps<KS, M>::group_tiles(a) * u.steps;
+        u.steps = S::of_pages(a);
+        total = a.b.tokens * a.heads * S::group_tiles(a) * u.steps;
     } else {
-        total = find_run<KS, M, WORKERS, kBlock>(a, reinterpret_cast<int64_t*>(ws), run);
+        total = find_run<S, WORKERS, kBlock>(a, reinterpret_cast<int64_t*>(ws), run);
     }
-    const Shares<WORKERS> sh(total);
+    const Shares<WORKERS> sh(total, S::kMost);
     const int32_t me = sh.me();
     if (me >= sh.workers) return;
     at = sh.begin(me);
@@ -72,28 +73,23 @@ __global__ void __launch_bounds__(kBlock, 2) attention_kernel(AttnArgs a) {
         int32_t last = 0;  // selected pages: the token's own position
         bool real = true;
         if constexpr (SPARSE) {
-            const int32_t tiles = Steps<KS, M>::group_tiles(a);
+            const int32_t tiles = S::group_tiles(a);
             const int64_t n = at / u.steps;
-            u.first = n * u.steps;
-            const int32_t tile = (int32_t)(n % tiles);
             const int64_t th = n / tiles;
             u.h = (int32_t)(th % a.heads);
             u.tok = th / a.heads;
+            S::place(u, a.group, n % tiles * M, th * tiles * u.steps);
             u.s = seq_of_token(a.b, u.tok);
             q = seq_info(a.b, a.pg, u.s);
             const int64_t i = u.tok - q.start;
             real = i >= 0 && i < q.len;  // a token behind the last sequence has no output
             last = (int32_t)min((int64_t)(a.pg.max_blocks << a.pg.shift) - 1, (int64_t)q.ctx + i);
-            u.row0 = tile * M;
-            u.rows = min(M, a.group - u.row0);
         } else {
-            unit_of_step<KS, M>(a, at, u, q, seq_first);
+            unit_at<S>(a, at, u, q, seq_first);
         }
         const int64_t tok = u.tok;  // the first token of its rows
-        const int32_t step0 = (int32_t)(at - u.first);
-        const int64_t unit_end = u.first + u.steps;
-        const int32_t step1 = (int32_t)((end < unit_end ? end : unit_end) - u.first);
-        at = u.first + step1;
+        const int32_t step0 = u.step_at(at), step1 = u.step_at(end);
+        at = u.end();
         if (!real) continue;
 
         // Query row r of the unit: token and query head (rows past the last repeat it).
@@ -406,8 +402,8 @@ hipError_t run(const AttnArgs& a, hipStream_t st) {
     else attention_kernel<E, MX, D, R, SPARSE, false><<<kWorkers, kBlock, 0, st>>>(a);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
-    constexpr int KS = 16 * Tile<E, MX, D>::SUB * kWaves;
-    return launch_join<E, D, KS, 16 * R, kWorkers, SPARSE>(a, st);
+    using S = Steps<16 * Tile<E, MX, D>::SUB * kWaves, 16 * R, 0>;
+    return launch_join<E, D, S, kWorkers, SPARSE>(a, st);
 }
 
 template <class E, bool MX, int D, bool SPARSE>

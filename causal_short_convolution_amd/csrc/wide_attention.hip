@@ -19,6 +19,9 @@ namespace sc {
 namespace {
 
 constexpr int kKeys = 64;  // keys per step
+// What a step costs beside its tiles of 16 query rows, in the cost of one tile. Measured on 131072 keys
+// of 8 heads: steps of 2.9 us with 16 tiles, of 2.0 us with one.
+constexpr int kLoadCost = 32;
 
 template <int D>
 struct Places {
@@ -75,6 +78,7 @@ __global__ void __launch_bounds__(64 * NW, D == 256 && NW == 4 ? 1 : 2) wide_ker
     constexpr int NT = 64 * NW;
     constexpr int M = 16 * R * NW;
     constexpr int WORKERS = wide_workers(NW, D);
+    using S = Steps<kKeys, M, kLoadCost>;
     using PC = Pieces<MX, D, NW>;
     __shared__ __attribute__((aligned(16))) char kbuf[2][PL::K_BYTES];
     __shared__ __attribute__((aligned(16))) char vbuf[2][PL::V_BYTES];
@@ -88,8 +92,8 @@ __global__ void __launch_bounds__(64 * NW, D == 256 && NW == 4 ? 1 : 2) wide_ker
     const uint32_t row_bytes = (uint32_t)(a.heads * D * EB);
     char* ws = static_cast<char*>(a.ws);
 
-    const int64_t total = find_run<kKeys, M, WORKERS, NT>(a, reinterpret_cast<int64_t*>(ws), run);
-    const Shares<WORKERS> sh(total);
+    const int64_t total = find_run<S, WORKERS, NT>(a, reinterpret_cast<int64_t*>(ws), run);
+    const Shares<WORKERS> sh(total, S::kMost);
     const int32_t me = sh.me();
     if (me >= sh.workers) return;
     int64_t at = sh.begin(me);
@@ -101,11 +105,10 @@ __global__ void __launch_bounds__(64 * NW, D == 256 && NW == 4 ? 1 : 2) wide_ker
     const float to_log2 = logit_factor(a.scale);
 
     while (at < end) {
-        unit_of_step<kKeys, M>(a, at, u, q, seq_first);
-        const int32_t step0 = (int32_t)(at - u.first);
-        const int64_t unit_end = u.first + u.steps;
-        const int32_t step1 = (int32_t)((end < unit_end ? end : unit_end) - u.first);
-        at = u.first + step1;
+        unit_at<S>(a, at, u, q, seq_first);
+        const int32_t step0 = u.step_at(at), step1 = u.step_at(end);
+        at = u.end();
+        if (step0 == step1) continue;  // the unit's last step started in the run before
 
         // Row tiles go round the waves: tile wave + NW r is the wave's r-th.
         const int tiles = (u.rows + 15) / 16;
@@ -474,7 +477,8 @@ hipError_t run(const AttnArgs& a, hipStream_t st) {
     wide_kernel<MX, D, NW, R><<<wide_workers(NW, D), 64 * NW, 0, st>>>(a);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
-    return launch_join<BF16, D, kKeys, 16 * R * NW, wide_workers(NW, D), false>(a, st);
+    using S = Steps<kKeys, 16 * R * NW, kLoadCost>;
+    return launch_join<BF16, D, S, wide_workers(NW, D), false>(a, st);
 }
 
 template <bool MX, int D>
