@@ -320,6 +320,8 @@ int summary(const char* fn, bool mx, const void* k, const void* ks, const int32_
     return launched(fn, sc::launch_block_summary(a, mx, dtype, D, (hipStream_t)stream));
 }
 
+int64_t key_stride(int32_t max_blocks) { return ((int64_t)max_blocks + 3) / 4 * 4; }
+
 // Rows that can have to move for one head: none unless an entry lies past the budget.
 int64_t most_moves(int64_t capacity, int32_t budget) {
     const int64_t past = capacity > budget ? capacity - budget : 0;
@@ -490,7 +492,7 @@ SC_API size_t shortconv_block_select_workspace_size(int64_t total_tokens, int32_
     g_err[0] = 0;
     if (total_tokens < 0 || total_tokens > INT32_MAX || max_blocks < 0 || num_heads < 1)
         return bad_size(fn, "bad total_tokens, max_blocks or num_heads");
-    return (size_t)total_tokens * num_heads * max_blocks * sizeof(uint32_t);
+    return (size_t)total_tokens * num_heads * key_stride(max_blocks) * sizeof(uint32_t);
 }
 
 SC_API int shortconv_block_select(const void* q, int64_t q_tok_stride, const int32_t* cu_seqlens,
@@ -520,7 +522,8 @@ SC_API int shortconv_block_select(const void* q, int64_t q_tok_stride, const int
         return fail(SC_ERR_INVALID, "%s: null summary or exponents", fn);
     const void* ptrs[] = {q, summary_, workspace};
     SC_TRY(check_aligned(fn, ptrs, 3));
-    const size_t need = (size_t)total_tokens * num_heads * max_blocks * sizeof(uint32_t);
+    const size_t need =
+        (size_t)total_tokens * num_heads * key_stride(max_blocks) * sizeof(uint32_t);
     if (need > 0 && (!workspace || workspace_bytes < need))
         return fail(SC_ERR_INVALID, "%s: workspace of %zu bytes needed, %zu given", fn, need,
                     workspace ? workspace_bytes : (size_t)0);
@@ -533,6 +536,7 @@ SC_API int shortconv_block_select(const void* q, int64_t q_tok_stride, const int
     a.exponents = static_cast<const uint8_t*>(exponents);
     a.selected = selected;
     a.keys = static_cast<uint32_t*>(workspace);
+    a.key_stride = key_stride(max_blocks);
     a.topk = topk;
     a.sinks = sink_blocks;
     a.recents = recent_blocks;

@@ -118,79 +118,219 @@ __global__ void __launch_bounds__(kBlock) summary_kernel(SummaryArgs a) {
     }
 }
 
-// One workgroup per (token, cache head): the query's codes, a score for every page, the k-th
-// largest score, and the chosen pages in order.
-template <class E, int D>
-__global__ void __launch_bounds__(kBlock) select_kernel(SelectArgs a) {
-    __shared__ uint32_t hist[258];
-    __shared__ int sums[8];
-    __shared__ int box[2][D];  // sums over the heads of the codes below and above zero
-    __shared__ uint32_t tops[4];
-    const int64_t t = blockIdx.x;
+// ------------------------------------------------------------------------------------------------
+// Scores. sum_d max(c min_d, c max_d) is the product of the page's row [minima, maxima] with the
+// query's [codes below zero, codes above zero], so the score of a page is one dot product of 2 D
+// bytes, and of 16 pages against 16 tokens one chain of 16x16x64 int8 matrix products. The query
+// heads that read one cache head are summed before: codes up to 127 G in PLANES planes of 6 bits (the
+// top one signed), whose products are put together as whole numbers.
+// ------------------------------------------------------------------------------------------------
+typedef int32_t i32x4 __attribute__((ext_vector_type(4)));
+constexpr int kTokens = 16;  // tokens of one sequence per workgroup
+
+template <class E>
+__device__ inline float query_element(const char* base, int j) {  // a NaN counts as 0
+    const float f = E::BYTES == 4
+                        ? reinterpret_cast<const float*>(base)[j]
+                        : __uint_as_float((uint32_t) reinterpret_cast<const uint16_t*>(base)[j] << 16);
+    return f != f ? 0.0f : f;
+}
+
+// Workgroup: tile blockIdx.x of kTokens tokens (tiles do not cross sequences), head blockIdx.y,
+// every gridDim.z-th group of 4 x 16 pages.
+template <class E, int D, int PLANES>
+__global__ void __launch_bounds__(kBlock) score_kernel(SelectArgs a) {
+    constexpr int ROW = 2 * D;  // bytes of a page's row
+    constexpr int NF = ROW / 64;
+    __shared__ __attribute__((aligned(16))) int8_t code[PLANES][kTokens][ROW + 16];
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int wave = uniform(tid >> 6);
+    const int c = lane & 15, g = lane >> 4;
     const int h = blockIdx.y;
+    const int64_t tile = blockIdx.x;
+    const int s = find_tile_seq<kTokens>(a.b.cu, a.b.num_seqs, a.b.tokens, tile);
+    const SeqInfo q = seq_info(a.b, a.pg, s);
+    const int64_t i0 = (tile - tile_base<kTokens>(a.b.cu, s, a.b.tokens)) * kTokens;
+    if (i0 < 0 || i0 >= q.len) return;
+    const int n = (int)min((int64_t)kTokens, q.len - i0);
+    const int64_t t0 = q.start + i0;
+
+    // ---- the tokens' codes: 4 tokens per wave, one after the other
+    for (int k = wave; k < kTokens; k += 4) {
+        const char* base = static_cast<const char*>(a.q) +
+                           ((t0 + min(k, n - 1)) * a.q_stride + (int64_t)h * a.group * D) * E::BYTES;
+        uint32_t top = 0;
+        for (int j = lane; j < a.group * D; j += 64)
+            top = max(top, __float_as_uint(__builtin_fabsf(query_element<E>(base, j))));
+        const int e = code_exponent(head_max<64>(top));
+        for (int d = lane; d < D; d += 64) {
+            int below = 0, above = 0;
+            for (int x = 0; x < a.group; ++x) {
+                const int v = (int)code_of(query_element<E>(base, x * D + d), e);
+                below += min(v, 0);
+                above += max(v, 0);
+            }
+#pragma unroll
+            for (int p = 0; p < PLANES; ++p) {
+                const bool last = p == PLANES - 1;
+                code[p][k][d] = (int8_t)(last ? below >> (6 * p) : (below >> (6 * p)) & 63);
+                code[p][k][D + d] = (int8_t)(last ? above >> (6 * p) : (above >> (6 * p)) & 63);
+            }
+        }
+    }
+    __syncthreads();
+    i32x4 qc[PLANES][NF];
+#pragma unroll
+    for (int p = 0; p < PLANES; ++p)
+#pragma unroll
+        for (int f = 0; f < NF; ++f)
+            qc[p][f] = *reinterpret_cast<const i32x4*>(&code[p][c][f * 64 + g * 16]);
+
+    // ---- 16 pages at a time: the lane gets token c's scores of pages 4 g + i
+    const int32_t* table = a.pg.table + (int64_t)s * a.pg.max_blocks;
+    const int64_t last_pos = (int64_t)q.ctx + i0 + n - 1;
+    const int32_t pages = (int32_t)min((int64_t)a.pg.max_blocks, (last_pos >> a.pg.shift) + 1);
+    const int32_t own = (int32_t)min((int64_t)a.pg.max_blocks,
+                                     (((int64_t)q.ctx + i0 + c) >> a.pg.shift) + 1);
+    uint32_t* keys = a.keys + ((t0 + c) * a.heads + h) * a.key_stride;
+    for (int32_t p0 = (blockIdx.z * 4 + wave) * 16; p0 < pages; p0 += gridDim.z * 64) {
+        const int32_t pb = p0 + c;
+        const int32_t page = pb < pages ? table[pb] : -1;
+        const bool ok = page >= 0 && page < a.pg.num_pages;
+        const int64_t at = (int64_t)(ok ? page : 0) * a.heads + h;
+        i32x4 row[NF];
+        int e = 0;
+        if (a.pg.num_pages > 0) {  // (a pool with pages has a page 0)
+#pragma unroll
+            for (int f = 0; f < NF; ++f)
+                row[f] = *reinterpret_cast<const i32x4*>(a.summary + at * ROW + f * 64 + g * 16);
+            e = (int)a.exponents[at] - 127;
+        } else {
+#pragma unroll
+            for (int f = 0; f < NF; ++f) row[f] = i32x4{0, 0, 0, 0};
+        }
+        i32x4 sum = {0, 0, 0, 0};
+#pragma unroll
+        for (int p = PLANES - 1; p >= 0; --p) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) sum[i] = (int32_t)((uint32_t)sum[i] << 6);
+#pragma unroll
+            for (int f = 0; f < NF; ++f)
+                sum = __builtin_amdgcn_mfma_i32_16x16x64_i8(row[f], qc[p][f], sum, 0, 0, 0);
+        }
+        uint32_t key[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int32_t b = p0 + g * 4 + i;
+            const int eb = __shfl(e, g * 4 + i);
+            const bool usable = __shfl((int)ok, g * 4 + i);
+            const bool forced = b < a.sinks || b >= (int64_t)own - a.recents;
+            key[i] = forced ? 0xffffffffu : order_key(__builtin_ldexpf((float)sum[i], eb));
+            if (!usable || b >= own) key[i] = 0;  // below every score: never chosen
+        }
+        if (c < n) {  // (rows of keys are padded to whole groups of 4)
+            if (p0 + g * 4 < pages)
+                *reinterpret_cast<uint4*>(keys + p0 + g * 4) =
+                    make_uint4(key[0], key[1], key[2], key[3]);
+        }
+    }
+}
+
+// ------------------------------------------------------------------------------------------------
+// The pages with the largest keys, one workgroup per (token, cache head).
+// ------------------------------------------------------------------------------------------------
+__device__ inline int token_pages(const SelectArgs& a, int64_t t) {
     const int s = seq_of_token(a.b, t);
     const SeqInfo q = seq_info(a.b, a.pg, s);
     const int64_t i = t - q.start;
-    if (i < 0 || i >= q.len) return;
-    const int tid = threadIdx.x;
-    const char* base = static_cast<const char*>(a.q) +
-                       (t * a.q_stride + (int64_t)h * a.group * D) * E::BYTES;
-    auto element = [&](int j) {
-        const float f = E::BYTES == 4
-                            ? reinterpret_cast<const float*>(base)[j]
-                            : __uint_as_float((uint32_t) reinterpret_cast<const uint16_t*>(base)[j] << 16);
-        return f != f ? 0.0f : f;
-    };
-    uint32_t top = 0;
-    for (int j = tid; j < a.group * D; j += kBlock)
-        top = max(top, __float_as_uint(__builtin_fabsf(element(j))));
-    top = head_max<64>(top);
-    if ((tid & 63) == 0) tops[tid >> 6] = top;
-    __syncthreads();
-    const int e = code_exponent(max(max(tops[0], tops[1]), max(tops[2], tops[3])));
-    for (int d = tid; d < D; d += kBlock) {
-        int below = 0, above = 0;
-        for (int g = 0; g < a.group; ++g) {
-            const int c = (int)code_of(element(g * D + d), e);
-            below += min(c, 0);
-            above += max(c, 0);
-        }
-        box[0][d] = below;
-        box[1][d] = above;
-    }
-    __syncthreads();
+    if (i < 0 || i >= q.len) return -1;
+    const int64_t all = (((int64_t)q.ctx + i) >> a.pg.shift) + 1;
+    return (int)(all < a.pg.max_blocks ? all : a.pg.max_blocks);
+}
 
-    const int64_t pos = (int64_t)q.ctx + i;
-    const int64_t all = (pos >> a.pg.shift) + 1;
-    const int P = (int)(all < a.pg.max_blocks ? all : a.pg.max_blocks);
-    uint32_t* keys = a.keys + (t * a.heads + h) * a.pg.max_blocks;
-    const int32_t* table = a.pg.table + (int64_t)s * a.pg.max_blocks;
-    int usable = 0;
-    for (int pb = tid; pb < P; pb += kBlock) {
-        const int32_t page = table[pb];
-        uint32_t key = 0;  // below every score: never chosen
-        if (page >= 0 && page < a.pg.num_pages) {
-            ++usable;
-            if (pb < a.sinks || pb >= (int64_t)P - a.recents) {
-                key = 0xffffffffu;
-            } else {
-                const int64_t at = (int64_t)page * a.heads + h;
-                const uint32_t* row = reinterpret_cast<const uint32_t*>(a.summary + at * 2 * D);
-                const int* w = &box[0][0];
-                int sum = 0;
-                for (int j = 0; j < D / 2; ++j) {
-                    const uint32_t x = row[j];
-                    sum += (int)(int8_t)(x) * w[4 * j] + (int)(int8_t)(x >> 8) * w[4 * j + 1] +
-                           (int)(int8_t)(x >> 16) * w[4 * j + 2] + (int)(int8_t)(x >> 24) * w[4 * j + 3];
-                }
-                key = order_key(__builtin_ldexpf((float)sum, (int)a.exponents[at] - 127));
-            }
-        }
-        keys[pb] = key;
+// Up to KPT keys per thread in registers, key i * THREADS + tid in register i.
+template <int THREADS, int KPT>
+__global__ void __launch_bounds__(THREADS) pick_kernel(SelectArgs a) {
+    constexpr int WAVES = THREADS / 64;
+    static_assert(KPT * WAVES <= THREADS, "one count per thread");
+    __shared__ KthScratch scratch;
+    __shared__ int sums[WAVES + 1];
+    __shared__ int first[2][KPT * WAVES];
+    const int64_t t = blockIdx.x;
+    const int h = blockIdx.y, tid = threadIdx.x;
+    const int wave = uniform(tid >> 6);
+    const int P = token_pages(a, t);
+    if (P < 0) return;  // a token behind the last sequence
+    const uint32_t* keys = a.keys + (t * a.heads + h) * a.key_stride;
+    int32_t* out = a.selected + (t * a.heads + h) * a.topk;
+    uint32_t key[KPT];
+#pragma unroll
+    for (int i = 0; i < KPT; ++i) {
+        const int j = i * THREADS + tid;
+        key[i] = P > 0 ? keys[min(j, P - 1)] : 0u;
+        if (j >= P) key[i] = 0;
     }
-    int total;
+    const int usable = count_at_least<THREADS, KPT>(key, 1u, 0, scratch);
+    __syncthreads();
+    const int k = min(a.topk, usable);
+    int total = 0, done = 0;
+    if (k > 0) {
+        uint32_t threshold;
+        int ties;
+        kth_of_registers<THREADS, KPT>(key, P, k, scratch, threshold, ties);
+        auto below = [](uint64_t mask) {  // bits of lower lanes
+            return (int)__builtin_amdgcn_mbcnt_hi((uint32_t)(mask >> 32),
+                                                  __builtin_amdgcn_mbcnt_lo((uint32_t)mask, 0));
+        };
+        auto scan = [&](int list) {  // counts of (i, wave) to places
+            __syncthreads();
+            const int n = tid < KPT * WAVES ? first[list][tid] : 0;
+            const int x = block_prefix(n, sums, total);
+            if (tid < KPT * WAVES) first[list][tid] = x;
+            __syncthreads();
+            return total;
+        };
+        if (ties > 0) {  // the lowest of the equal pages
+#pragma unroll
+            for (int i = 0; i < KPT; ++i) {
+                const uint64_t m = __ballot(key[i] == threshold);
+                if ((tid & 63) == 0) first[0][i * WAVES + wave] = __builtin_popcountll(m);
+            }
+            scan(0);
+        }
+#pragma unroll
+        for (int i = 0; i < KPT; ++i) {
+            bool keep = key[i] > threshold;
+            if (ties > 0) {
+                const bool tie = key[i] == threshold;
+                keep |= tie && first[0][i * WAVES + wave] + below(__ballot(tie)) < ties;
+            }
+            const uint64_t m = __ballot(keep);
+            if ((tid & 63) == 0) first[1][i * WAVES + wave] = __builtin_popcountll(m);
+            key[i] = keep;
+        }
+        done = scan(1);
+#pragma unroll
+        for (int i = 0; i < KPT; ++i) {
+            const uint64_t m = __ballot(key[i] != 0);
+            if (key[i]) out[first[1][i * WAVES + wave] + below(m)] = i * THREADS + tid;
+        }
+    }
+    for (int j = done + tid; j < a.topk; j += THREADS) out[j] = -1;
+}
+
+// More pages than registers hold.
+__global__ void __launch_bounds__(kBlock) pick_long_kernel(SelectArgs a) {
+    __shared__ uint32_t hist[258];
+    __shared__ int sums[kBlock / 64 + 1];
+    const int64_t t = blockIdx.x;
+    const int h = blockIdx.y, tid = threadIdx.x;
+    const int P = token_pages(a, t);
+    if (P < 0) return;
+    const uint32_t* keys = a.keys + (t * a.heads + h) * a.key_stride;
+    int usable = 0, total;
+    for (int j = tid; j < P; j += kBlock) usable += keys[j] != 0;
     block_prefix(usable, sums, total);
-    __syncthreads();  // the keys of every thread are written
     const int k = min(a.topk, total);
     uint32_t threshold = 1;
     int ties = 0;
@@ -233,7 +373,25 @@ hipError_t summary_by_dim(const SummaryArgs& a, int D, hipStream_t st) {
 
 template <class E, int D>
 hipError_t run_select(const SelectArgs& a, hipStream_t st) {
-    select_kernel<E, D><<<dim3((uint32_t)a.b.tokens, (uint32_t)a.heads), kBlock, 0, st>>>(a);
+    const int64_t tiles = a.b.tokens / kTokens + a.b.num_seqs;
+    // Workgroups share the pages of a tile where there are few tiles.
+    const int64_t groups = ((int64_t)a.pg.max_blocks + 63) / 64;
+    int64_t share = 1024 / (tiles * a.heads) + 1;
+    share = share < groups ? share : groups;
+    if (share > 0) {
+        const dim3 grid((uint32_t)tiles, (uint32_t)a.heads, (uint32_t)share);
+        // 127 G of a code's sum in planes of 6 bits and a signed one of 7
+        if (a.group <= 64) score_kernel<E, D, 2><<<grid, kBlock, 0, st>>>(a);
+        else score_kernel<E, D, 3><<<grid, kBlock, 0, st>>>(a);
+        const hipError_t e = hipGetLastError();
+        if (e != hipSuccess) return e;
+    }
+    const dim3 each((uint32_t)a.b.tokens, (uint32_t)a.heads);
+    const int32_t n = a.pg.max_blocks;
+    if (n <= 16 * 64) pick_kernel<64, 16><<<each, 64, 0, st>>>(a);
+    else if (n <= 16 * 256) pick_kernel<256, 16><<<each, 256, 0, st>>>(a);
+    else if (n <= 64 * 256) pick_kernel<256, 64><<<each, 256, 0, st>>>(a);
+    else pick_long_kernel<<<each, kBlock, 0, st>>>(a);
     return hipGetLastError();
 }
 

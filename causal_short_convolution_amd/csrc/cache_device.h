@@ -203,6 +203,7 @@ __device__ inline void kth_of_registers(const uint32_t (&key)[KPT], int n, int k
     int above = 0;    // keys past those that can still be the k-th largest
     int reach = n;    // keys at or above t
     int bit = 31;
+    __syncthreads();
     if (threadIdx.x == 0) sc.used = sc.differ = 0;
     for (; bit >= 0 && reach - above > KthScratch::kList; --bit) {
         const uint32_t cand = t | (1u << bit);

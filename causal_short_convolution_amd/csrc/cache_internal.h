@@ -78,7 +78,8 @@ struct SelectArgs {
     const int8_t* summary;
     const uint8_t* exponents;
     int32_t* selected;  // [tokens][heads][topk]
-    uint32_t* keys;     // workspace [tokens][heads][max_blocks]
+    uint32_t* keys;     // workspace [tokens][heads][key_stride]
+    int64_t key_stride; // max_blocks, padded to whole groups of 4
     int32_t topk;
     int32_t sinks;
     int32_t recents;
