@@ -12,7 +12,7 @@
 //        rescaling of a row are per-lane values.
 // A contraction may run in any order, so K is loaded 16 bytes per lane straight into its operand
 // (key c, channels by g), and V 16 bytes per lane by rows (keys 4g + i, channels by c), transposed
-// in registers by byte permutes. Neither goes through LDS.
+// in registers by byte permutes. Neither goes through LDS; of an MXFP8 tile only the scales do.
 #ifndef SHORTCONV_ATTENTION_TILE_H
 #define SHORTCONV_ATTENTION_TILE_H
 
@@ -110,6 +110,44 @@ __device__ inline const char* key_row(const char* cache, const KeyTile<SUB, PAGE
     }
 }
 
+// The scale bytes of one tile's keys, D / 32 for each row of K and of V: lane l loads those of key
+// l % KW, of K (l < 32) or V, and leaves them in the wave's LDS as words [K, V][D / 128][KW], where
+// an operand finds the ones of its keys. (Loaded by each lane for its own operands they were 10 of a
+// step's 22 load instructions, and the address units' time bounded the step.)
+template <int SUB, int D>
+struct Scales {
+    static constexpr int KW = 16 * SUB, NW = (D + 127) / 128;
+    static constexpr int kWords = 2 * NW * KW;
+    uint32_t w[NW];
+
+    template <bool PG>
+    __device__ inline void load(const char* k, const char* v, const KeyTile<SUB, PG>& t,
+                                uint32_t row, int lane) {
+        int32_t r = t.base[0];
+        if constexpr (PG) r = (SUB == 2 && (lane & 16) ? t.base[SUB - 1] : r) + (lane & 15);
+        const char* p = (lane < 32 ? k : v) + (int64_t)r * row;
+        if constexpr (D == 64) {
+            w[0] = *reinterpret_cast<const uint16_t*>(p);
+        } else {
+#pragma unroll
+            for (int j = 0; j < NW; ++j) w[j] = *reinterpret_cast<const uint32_t*>(p + 4 * j);
+        }
+    }
+    __device__ inline void put(uint32_t* lds, int lane) const {
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+#pragma unroll
+        for (int j = 0; j < NW; ++j) lds[((lane >> 5) * NW + j) * KW + (lane & (KW - 1))] = w[j];
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    }
+    // Word j of K's key, and of V's keys 4 n ..
+    __device__ static inline uint32_t of_key(const uint32_t* lds, int j, int key) {
+        return lds[j * KW + key];
+    }
+    __device__ static inline uint4 of_values(const uint32_t* lds, int j, int n) {
+        return *reinterpret_cast<const uint4*>(lds + (NW + j) * KW + n * 4);
+    }
+};
+
 template <class E, bool MX, int D>
 struct Tile;
 
@@ -129,11 +167,9 @@ struct Tile<BF16, MX, D> {
 
     struct K {
         uint4 x[SUB][KN];
-        uint32_t s[SUB][MX ? (D + 127) / 128 : 1];
     };
     struct V {
         uint32_t x[SUB * 4][NU][MX ? CH / 4 : CH / 2];
-        uint8_t s[SUB * 4][MX ? NU : 1];
     };
     using Q = bf16x8[NF];
 
@@ -148,30 +184,18 @@ struct Tile<BF16, MX, D> {
     }
 
     template <bool PG>
-    __device__ static inline void load_k(const char* cache, const char* scales,
-                                         const KeyTile<SUB, PG>& t, uint32_t row, int c, int g,
-                                         K& k) {
+    __device__ static inline void load_k(const char* cache, const KeyTile<SUB, PG>& t,
+                                         uint32_t row, int c, int g, K& k) {
 #pragma unroll
         for (int s = 0; s < SUB; ++s) {
             const char* r = key_row(cache, t, s, s * 16 + c, row) + g * 16;
 #pragma unroll
             for (int f = 0; f < KN; ++f) k.x[s][f] = *reinterpret_cast<const uint4*>(r + f * 64);
-            if constexpr (MX) {
-                const char* e = key_row(scales, t, s, s * 16 + c, row / 32);
-                if constexpr (D == 64) {
-                    k.s[s][0] = *reinterpret_cast<const uint16_t*>(e);
-                } else {
-#pragma unroll
-                    for (int j = 0; j < D / 128; ++j)
-                        k.s[s][j] = *reinterpret_cast<const uint32_t*>(e + 4 * j);
-                }
-            }
         }
     }
     template <bool PG>
-    __device__ static inline void load_v(const char* cache, const char* scales,
-                                         const KeyTile<SUB, PG>& t, uint32_t row, int c, int g,
-                                         V& v) {
+    __device__ static inline void load_v(const char* cache, const KeyTile<SUB, PG>& t,
+                                         uint32_t row, int c, int g, V& v) {
 #pragma unroll
         for (int j = 0; j < SUB * 4; ++j) {
             const int key = (j >> 2) * 16 + g * 4 + (j & 3);
@@ -187,8 +211,6 @@ struct Tile<BF16, MX, D> {
                     } else {
                         v.x[j][u][0] = *reinterpret_cast<const uint32_t*>(p);
                     }
-                    v.s[j][u] = *reinterpret_cast<const uint8_t*>(
-                        key_row(scales, t, j >> 2, key, row / 32) + (u * 16 * CH + c * CH) / 32);
                 } else {
                     const char* p = r + (u * 16 * CH + c * CH) * 2;
                     if constexpr (CH == 8) {
@@ -213,14 +235,20 @@ struct Tile<BF16, MX, D> {
                   : __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(
                                                      w, scale, false));
     }
-    // The K operands of subtile s.
-    __device__ static inline void k_operands(const K& k, int s, int g, bf16x8 (&a)[NF]) {
+    // The K operands of subtile s; `sc`: the tile's scales in LDS.
+    __device__ static inline void k_operands(const K& k, const uint32_t* sc, int s, int c, int g,
+                                             bf16x8 (&a)[NF]) {
+        uint32_t words[MX ? Scales<SUB, D>::NW : 1];
+        if constexpr (MX) {
+#pragma unroll
+            for (int j = 0; j < Scales<SUB, D>::NW; ++j)
+                words[j] = Scales<SUB, D>::of_key(sc, j, s * 16 + c);
+        }
 #pragma unroll
         for (int f = 0; f < KN; ++f) {
             if constexpr (MX) {
                 // 16 channels f * 64 + 16 g ..: scale byte 2 f + g / 2 of the row
-                const uint32_t word = k.s[s][f / 2];
-                const float e = e8m0((word >> ((f & 1) * 16 + (g >> 1) * 8)) & 255u);
+                const float e = e8m0((words[f / 2] >> ((f & 1) * 16 + (g >> 1) * 8)) & 255u);
                 const uint32_t w[4] = {k.x[s][f].x, k.x[s][f].y, k.x[s][f].z, k.x[s][f].w};
 #pragma unroll
                 for (int p = 0; p < 2; ++p) {
@@ -247,13 +275,27 @@ struct Tile<BF16, MX, D> {
     struct VOp {
         uint32_t w[SUB * 4][NU][CH / 2];
     };
-    __device__ static inline void v_operands(const V& v, VOp& o) {
+    __device__ static inline void v_operands(const V& v, const uint32_t* sc, int c, int g, VOp& o) {
+        uint32_t words[SUB * 4][MX ? Scales<SUB, D>::NW : 1];
+        if constexpr (MX) {
+#pragma unroll
+            for (int s = 0; s < SUB; ++s)
+#pragma unroll
+                for (int k = 0; k < Scales<SUB, D>::NW; ++k) {
+                    const uint4 w = Scales<SUB, D>::of_values(sc, k, s * 4 + g);
+                    words[s * 4][k] = w.x;
+                    words[s * 4 + 1][k] = w.y;
+                    words[s * 4 + 2][k] = w.z;
+                    words[s * 4 + 3][k] = w.w;
+                }
+        }
 #pragma unroll
         for (int j = 0; j < SUB * 4; ++j)
 #pragma unroll
             for (int u = 0; u < NU; ++u) {
                 if constexpr (MX) {
-                    const float e = e8m0(v.s[j][u]);
+                    // channels u * 16 CH + c * CH ..: at CH 8 a word of scales per piece
+                    const float e = e8m0((words[j][u] >> ((CH == 8 ? c >> 2 : c >> 3) * 8)) & 255u);
 #pragma unroll
                     for (int q = 0; q < CH / 4; ++q) {
                         o.w[j][u][2 * q] = widen2(v.x[j][u][q], e, false);
@@ -330,11 +372,9 @@ struct Tile<F32, MX, D> {
 
     struct K {
         uint4 x[KN];
-        uint32_t s[MX ? (D + 127) / 128 : 1];
     };
     struct V {
         uint32_t x[4][NU][MX ? 1 : 4];
-        uint8_t s[4][MX ? NU : 1];
     };
     using Q = f32x4[NF];
 
@@ -347,27 +387,15 @@ struct Tile<F32, MX, D> {
             q[f] = *reinterpret_cast<const f32x4*>(row + q_channel(f, g) * QB);
     }
     template <bool PG>
-    __device__ static inline void load_k(const char* cache, const char* scales,
-                                         const KeyTile<SUB, PG>& t, uint32_t row, int c, int g,
-                                         K& k) {
+    __device__ static inline void load_k(const char* cache, const KeyTile<SUB, PG>& t,
+                                         uint32_t row, int c, int g, K& k) {
         const char* r = key_row(cache, t, 0, c, row) + g * 16;
 #pragma unroll
         for (int f = 0; f < KN; ++f) k.x[f] = *reinterpret_cast<const uint4*>(r + f * 64);
-        if constexpr (MX) {
-            const char* e = key_row(scales, t, 0, c, row / 32);
-            if constexpr (D == 64) {
-                k.s[0] = *reinterpret_cast<const uint16_t*>(e);
-            } else {
-#pragma unroll
-                for (int j = 0; j < D / 128; ++j)
-                    k.s[j] = *reinterpret_cast<const uint32_t*>(e + 4 * j);
-            }
-        }
     }
     template <bool PG>
-    __device__ static inline void load_v(const char* cache, const char* scales,
-                                         const KeyTile<SUB, PG>& t, uint32_t row, int c, int g,
-                                         V& v) {
+    __device__ static inline void load_v(const char* cache, const KeyTile<SUB, PG>& t,
+                                         uint32_t row, int c, int g, V& v) {
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             const char* r = key_row(cache, t, 0, g * 4 + j, row);
@@ -375,8 +403,6 @@ struct Tile<F32, MX, D> {
             for (int u = 0; u < NU; ++u) {
                 if constexpr (MX) {
                     v.x[j][u][0] = *reinterpret_cast<const uint32_t*>(r + u * 64 + c * 4);
-                    v.s[j][u] = *reinterpret_cast<const uint8_t*>(
-                        key_row(scales, t, 0, g * 4 + j, row / 32) + (u * 64 + c * 4) / 32);
                 } else {
                     const uint4 w = *reinterpret_cast<const uint4*>(r + (u * 64 + c * 4) * 4);
                     v.x[j][u][0] = w.x;
@@ -388,11 +414,17 @@ struct Tile<F32, MX, D> {
         }
     }
     using KOp = f32x4[NF];
-    __device__ static inline void k_operands(const K& k, int, int g, KOp& a) {
+    __device__ static inline void k_operands(const K& k, const uint32_t* sc, int, int c, int g,
+                                             KOp& a) {
+        uint32_t words[MX ? Scales<SUB, D>::NW : 1];
+        if constexpr (MX) {
+#pragma unroll
+            for (int j = 0; j < Scales<SUB, D>::NW; ++j) words[j] = Scales<SUB, D>::of_key(sc, j, c);
+        }
 #pragma unroll
         for (int f = 0; f < KN; ++f) {
             if constexpr (MX) {
-                const float e = e8m0((k.s[f / 2] >> ((f & 1) * 16 + (g >> 1) * 8)) & 255u);
+                const float e = e8m0((words[f / 2] >> ((f & 1) * 16 + (g >> 1) * 8)) & 255u);
                 const uint32_t w[4] = {k.x[f].x, k.x[f].y, k.x[f].z, k.x[f].w};
 #pragma unroll
                 for (int p = 0; p < 4; ++p) {
@@ -417,13 +449,25 @@ struct Tile<F32, MX, D> {
     struct VOp {
         float w[4][NU][4];
     };
-    __device__ static inline void v_operands(const V& v, VOp& o) {
+    __device__ static inline void v_operands(const V& v, const uint32_t* sc, int c, int g, VOp& o) {
+        uint32_t words[4][MX ? Scales<SUB, D>::NW : 1];
+        if constexpr (MX) {
+#pragma unroll
+            for (int k = 0; k < Scales<SUB, D>::NW; ++k) {
+                const uint4 w = Scales<SUB, D>::of_values(sc, k, g);
+                words[0][k] = w.x;
+                words[1][k] = w.y;
+                words[2][k] = w.z;
+                words[3][k] = w.w;
+            }
+        }
 #pragma unroll
         for (int j = 0; j < 4; ++j)
 #pragma unroll
             for (int u = 0; u < NU; ++u) {
                 if constexpr (MX) {
-                    const float e = e8m0(v.s[j][u]);
+                    // channels u * 64 + c * 4 ..: scale byte 2 u + c / 8 of the row
+                    const float e = e8m0((words[j][u / 2] >> ((u & 1) * 16 + (c >> 3) * 8)) & 255u);
                     const f32x2 lo = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(v.x[j][u][0], e, false);
                     const f32x2 hi = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(v.x[j][u][0], e, true);
                     o.w[j][u][0] = lo[0];

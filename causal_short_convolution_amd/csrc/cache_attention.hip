@@ -36,6 +36,8 @@ __global__ void __launch_bounds__(kBlock, 2) attention_kernel(AttnArgs a) {
     constexpr int kLds = 2 * M * OSTRIDE * 4 > M * QSTRIDE ? 2 * M * OSTRIDE * 4 : M * QSTRIDE;
     __shared__ __attribute__((aligned(16))) char lds[kLds];
     __shared__ float stat[kWaves][2][M];
+    using SC = Scales<SUB, D>;
+    __shared__ __attribute__((aligned(16))) uint32_t scale_lds[kWaves][MX ? SC::kWords : 1];
     __shared__ RunScratch run;
     __shared__ int32_t left_out_any;
 
@@ -193,8 +195,13 @@ __global__ void __launch_bounds__(kBlock, 2) attention_kernel(AttnArgs a) {
         int32_t step = step0;
         KT tile;
         bool more = next_tile(step, tile);
-        auto load_keys = [&](const KT& t) { T::load_k(kc, ks, t, row_bytes, c, g, kreg); };
-        auto load_values = [&](const KT& t) { T::load_v(vc, vs, t, row_bytes, c, g, vreg); };
+        SC sreg;
+        uint32_t* sc = scale_lds[wave];
+        auto load_keys = [&](const KT& t) {
+            if constexpr (MX) sreg.load(ks, vs, t, row_bytes / 32, lane);
+            T::load_k(kc, t, row_bytes, c, g, kreg);
+        };
+        auto load_values = [&](const KT& t) { T::load_v(vc, t, row_bytes, c, g, vreg); };
         if (AHEAD && more) {
             load_keys(tile);
             load_values(tile);
@@ -208,13 +215,14 @@ __global__ void __launch_bounds__(kBlock, 2) attention_kernel(AttnArgs a) {
                 load_keys(tile);
                 load_values(tile);
             }
+            if constexpr (MX) sreg.put(sc, lane);
             const int32_t k0 = step * KS + wave * KW;
             const uint32_t valid = tile.valid;
             f32x4 x[R][SUB];
 #pragma unroll
             for (int s = 0; s < SUB; ++s) {
                 typename T::KOp ko;
-                T::k_operands(kreg, s, g, ko);
+                T::k_operands(kreg, sc, s, c, g, ko);
 #pragma unroll
                 for (int r = 0; r < R; ++r) {
                     if constexpr (QREG) {
@@ -235,7 +243,7 @@ __global__ void __launch_bounds__(kBlock, 2) attention_kernel(AttnArgs a) {
             // rows; selected pages are one token's, seen alike by all its heads.
             const bool all_seen = valid == kFull && (SPARSE || k0 + KW <= q.ctx);
             typename T::VOp vo;
-            T::v_operands(vreg, vo);
+            T::v_operands(vreg, sc, c, g, vo);
             if (!all_seen) {
                 // Keys that do not exist have rows that hold anything. Among the new tokens a row
                 // of V may be one that only some query rows look at, and an infinity or a NaN

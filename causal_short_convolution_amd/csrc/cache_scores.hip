@@ -33,6 +33,8 @@ __global__ void __launch_bounds__(kBlock) scores_kernel(AttnArgs a) {
     constexpr int ROWS = D * T::QB * kRows > 65536 ? kRows / 2 : kRows;
     constexpr int QSTRIDE = D * T::QB + 16;
     __shared__ __attribute__((aligned(16))) char lds[ROWS * QSTRIDE];
+    using SC = Scales<SUB, D>;
+    __shared__ __attribute__((aligned(16))) uint32_t scale_lds[kWaves][MX ? SC::kWords : 1];
     __shared__ float norm[ROWS];  // lse in base 2; a row of -inf adds nothing
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = uniform(tid >> 6);
@@ -102,9 +104,16 @@ __global__ void __launch_bounds__(kBlock) scores_kernel(AttnArgs a) {
         typename T::KOp ko[SUB];
         if (tile.valid) {
             typename T::K kreg;
-            T::load_k(kc, ks, tile, row_bytes, c, g, kreg);
+            if constexpr (MX) {
+                SC sreg;
+                sreg.load(ks, ks, tile, row_bytes / 32, lane);
+                T::load_k(kc, tile, row_bytes, c, g, kreg);
+                sreg.put(scale_lds[wave], lane);
+            } else {
+                T::load_k(kc, tile, row_bytes, c, g, kreg);
+            }
 #pragma unroll
-            for (int x = 0; x < SUB; ++x) T::k_operands(kreg, x, g, ko[x]);
+            for (int x = 0; x < SUB; ++x) T::k_operands(kreg, scale_lds[wave], x, c, g, ko[x]);
         }
         for (int64_t r0 = 0; r0 < rows; r0 += ROWS) {
             if (!once) {
