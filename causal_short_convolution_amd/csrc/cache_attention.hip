@@ -103,23 +103,6 @@ __global__ void __launch_bounds__(kBlock, 2) attention_kernel(AttnArgs a) {
             const int32_t x = u.row0 + (r < u.rows ? r : u.rows - 1);
             return u.h * a.group + (SPARSE ? x : x % a.group);
         };
-        // ---- queries: to LDS, whole rows
-        __syncthreads();  // the last unit's use of LDS is over
-        if (tid == 0) left_out_any = 0;
-        {
-            constexpr int PIECES = D * T::QB / 16;
-            const char* qb = static_cast<const char*>(a.q);
-            for (int x = tid; x < M * PIECES; x += kBlock) {
-                const int r = x / PIECES, p = x % PIECES;
-                const int64_t off = row_token(r) * a.q_stride + (int64_t)row_head(r) * D;
-                *reinterpret_cast<uint4*>(lds + r * QSTRIDE + p * 16) = signed_by<E>(
-                    *reinterpret_cast<const uint4*>(qb + off * T::QB + p * 16), a.scale);
-            }
-        }
-        __syncthreads();
-        typename T::Q qreg;
-        if constexpr (QREG) T::load_q(lds + c * QSTRIDE, g, qreg);
-
         // ---- the wave's keys of one step
         const char* kc = static_cast<const char*>(a.cache[0]) + (int64_t)u.h * D * eb;
         const char* vc = static_cast<const char*>(a.cache[1]) + (int64_t)u.h * D * eb;
@@ -147,16 +130,26 @@ __global__ void __launch_bounds__(kBlock, 2) attention_kernel(AttnArgs a) {
             return (page << a.pg.shift) + (pos & ((1 << a.pg.shift) - 1));
         };
         using KT = KeyTile<SUB, PAGE16>;
+        // With PAGE16 the lanes look up the subtiles of the next kAhead steps at once, so the chain
+        // of loads (selected page, page table, keys) is waited for once in kAhead steps.
+        constexpr int kAhead = 64 / SUB;
+        int32_t found0 = step0 - kAhead, found_row = 0, found_keys = 0;
         auto locate = [&](int32_t step) {
             KT t;
             const int32_t k0 = step * KS + wave * KW;
             t.valid = 0;
             if constexpr (PAGE16) {
+                if (step >= found0 + kAhead) {
+                    found0 = step;
+                    found_row = found_keys = 0;
+                    if (step + lane / SUB < u.steps)
+                        found_row = find(k0 + lane / SUB * KS + lane % SUB * 16, found_keys);
+                }
 #pragma unroll
                 for (int s = 0; s < SUB; ++s) {
-                    int32_t exist;
-                    t.base[s] = uniform(find(k0 + s * 16, exist));
-                    exist = uniform(exist);
+                    const int from = (step - found0) * SUB + s;
+                    t.base[s] = __builtin_amdgcn_readlane(found_row, from);
+                    const int32_t exist = __builtin_amdgcn_readlane(found_keys, from);
                     const uint32_t bits = exist >= 16 ? 0xffffu : (1u << exist) - 1u;
                     t.valid |= bits << (16 * s);
                 }
@@ -206,8 +199,26 @@ __global__ void __launch_bounds__(kBlock, 2) attention_kernel(AttnArgs a) {
             load_keys(tile);
             load_values(tile);
         }
+        // ---- queries: to LDS, whole rows
+        __syncthreads();  // the last unit's use of LDS is over
+        if (tid == 0) left_out_any = 0;
+        {
+            constexpr int PIECES = D * T::QB / 16;
+            const char* qb = static_cast<const char*>(a.q);
+            for (int x = tid; x < M * PIECES; x += kBlock) {
+                const int r = x / PIECES, p = x % PIECES;
+                const int64_t off = row_token(r) * a.q_stride + (int64_t)row_head(r) * D;
+                *reinterpret_cast<uint4*>(lds + r * QSTRIDE + p * 16) = signed_by<E>(
+                    *reinterpret_cast<const uint4*>(qb + off * T::QB + p * 16), a.scale);
+            }
+        }
+        __syncthreads();
+        typename T::Q qreg;
+        if constexpr (QREG) T::load_q(lds + c * QSTRIDE, g, qreg);
+
         // Per step: logits from K, then the loads of the next K into the same registers, softmax
-        // and the product with V, then the loads of the next V. Where that takes more than half of
+        // and the product with V, then the loads of the next V (of MXFP8 as soon as this V has been
+        // widened). Where that takes more than half of
         // a SIMD's registers a step loads its own keys, and the other waves cover the wait.
         while (more) {
             if constexpr (!QREG) asm volatile("" ::: "memory");  // queries are read anew from LDS
@@ -244,6 +255,7 @@ __global__ void __launch_bounds__(kBlock, 2) attention_kernel(AttnArgs a) {
             const bool all_seen = valid == kFull && (SPARSE || k0 + KW <= q.ctx);
             typename T::VOp vo;
             T::v_operands(vreg, sc, c, g, vo);
+            if (AHEAD && MX && another) load_values(next);  // (widened: other registers)
             if (!all_seen) {
                 // Keys that do not exist have rows that hold anything. Among the new tokens a row
                 // of V may be one that only some query rows look at, and an infinity or a NaN
@@ -292,7 +304,7 @@ __global__ void __launch_bounds__(kBlock, 2) attention_kernel(AttnArgs a) {
                 }
                 T::values(vo, p, acc[r]);
             }
-            if (AHEAD && another) load_values(next);
+            if (AHEAD && !MX && another) load_values(next);
             more = another;
             step = next_step;
             tile = next;
