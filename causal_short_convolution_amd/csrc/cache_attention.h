@@ -9,7 +9,7 @@ namespace sc {
 // where the workgroup needs more than half of the CU's LDS or registers.
 constexpr int kWorkers = 512;
 constexpr int wide_workers(int waves, int head_dim) {
-    return waves == 4 && head_dim <= 128 ? 512 : 256;
+    return waves == 4 && head_dim <= 128 ? 768 : 256;
 }
 
 // How the query rows of a unit are held: waves = 0, every wave of a workgroup holds all rows, 16 x

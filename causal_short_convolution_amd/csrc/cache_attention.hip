@@ -63,7 +63,7 @@ __global__ void __launch_bounds__(kBlock, 2) attention_kernel(AttnArgs a) {
     at = sh.begin(me);
     end = sh.begin(me + 1);
     SeqInfo q;
-    int64_t seq_first = 0;
+    int64_t seq_first = 0, known = -1;  // selected pages: the token that q is of
     if constexpr (!SPARSE) {
         u.s = uniform(run.s);
         seq_first = uniform(run.first);
@@ -81,8 +81,11 @@ __global__ void __launch_bounds__(kBlock, 2) attention_kernel(AttnArgs a) {
             u.h = (int32_t)(th % a.heads);
             u.tok = th / a.heads;
             S::place(u, a.group, n % tiles * M, th * tiles * u.steps);
-            u.s = seq_of_token(a.b, u.tok);
-            q = seq_info(a.b, a.pg, u.s);
+            if (u.tok != known) {
+                u.s = seq_of_token(a.b, u.tok);
+                q = seq_info(a.b, a.pg, u.s);
+                known = u.tok;
+            }
             const int64_t i = u.tok - q.start;
             real = i >= 0 && i < q.len;  // a token behind the last sequence has no output
             last = (int32_t)min((int64_t)(a.pg.max_blocks << a.pg.shift) - 1, (int64_t)q.ctx + i);

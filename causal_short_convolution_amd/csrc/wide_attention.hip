@@ -7,7 +7,7 @@
 // K by rows, V transposed (rows of channels, keys in the order in which the lane of a query row
 // holds their weights), both in bf16 whatever the cache holds. Two such buffers alternate: while
 // step t is computed from one, step t + 1, loaded to registers a step earlier, is written to the
-// other, and the loads of step t + 2 are under way. One barrier per step.
+// other, and the loads of step t + 2 (with 4 waves, of t + 3 too) are under way. One barrier per step.
 //
 // Rows in LDS are not padded; their 16-byte pieces are permuted by exclusive or with bits of the row,
 // so that the lanes that an access serves at a time fall on different banks: 16 rows of one piece
@@ -63,15 +63,18 @@ struct Pieces {
     static constexpr int V0 = SPLIT ? 0 : K_WORDS;
     static constexpr int WORDS = !SPLIT ? K_WORDS + V_WORDS
                                         : K_WORDS > V_WORDS ? K_WORDS : V_WORDS;
-    static constexpr int E0 = SPLIT ? 0 : KN;       // scale bytes: KN of K, 4 VN of V
-    static constexpr int SCALES = !MX ? 1 : !SPLIT ? KN + 4 * VN : KN > 4 * VN ? KN : 4 * VN;
+    static constexpr int KK = 64 / KP, VK = 256 / VP;  // keys of a wave's n-th piece
     static_assert(KN * 256 == kKeys * KP && VN * 256 == kKeys / 4 * VP, "whole shares");
     uint32_t w[WORDS];
-    uint8_t e[SCALES];
+    // MXFP8: a wave's pieces are of 16 keys of K and 16 of V, whose scales its lanes load as words,
+    // one each (lane % 16 the key, lane / 32 the word; bit 4 says V where a wave loads both) and
+    // hand each other when the pieces are widened. Each lane loading its own bytes took half of all
+    // load instructions.
+    uint32_t scale;
 };
 
 template <bool MX, int D, int NW, int R>
-__global__ void __launch_bounds__(64 * NW, D == 256 && NW == 4 ? 1 : 2) wide_kernel(AttnArgs a) {
+__global__ void __launch_bounds__(64 * NW, D == 256 && NW == 4 ? 1 : NW == 4 ? 3 : 2) wide_kernel(AttnArgs a) {
     using T = Tile<BF16, false, D>;  // after staging the operands are bf16
     using X = Tile<BF16, MX, D>;
     using PL = Places<D>;
@@ -80,8 +83,9 @@ __global__ void __launch_bounds__(64 * NW, D == 256 && NW == 4 ? 1 : 2) wide_ker
     constexpr int WORKERS = wide_workers(NW, D);
     using S = Steps<kKeys, M, kLoadCost>;
     using PC = Pieces<MX, D, NW>;
-    __shared__ __attribute__((aligned(16))) char kbuf[2][PL::K_BYTES];
-    __shared__ __attribute__((aligned(16))) char vbuf[2][PL::V_BYTES];
+    constexpr int BUFS = NW == 4 && D <= 128 ? 1 : 2;
+    __shared__ __attribute__((aligned(16))) char kbuf[BUFS][PL::K_BYTES];
+    __shared__ __attribute__((aligned(16))) char vbuf[BUFS][PL::V_BYTES];
     __shared__ RunScratch run;
     __shared__ int32_t left_out_any;
 
@@ -164,7 +168,7 @@ __global__ void __launch_bounds__(64 * NW, D == 256 && NW == 4 ? 1 : 2) wide_ker
                                   (uint32_t)key * row_bytes
                             : (int64_t)((uint64_t)(uint32_t)__shfl(row, key) * row_bytes);
         };
-        auto load_k = [&](int32_t row) {
+        auto load_k = [&](PC& pc, int32_t row) {
 #pragma unroll
             for (int n = 0; n < PC::KN; ++n) {
                 const int x = n * 256 + t8;
@@ -172,10 +176,9 @@ __global__ void __launch_bounds__(64 * NW, D == 256 && NW == 4 ? 1 : 2) wide_ker
                 const u32x4 y = *reinterpret_cast<const u32x4*>(kc + r + x % PC::KP * 16);
 #pragma unroll
                 for (int i = 0; i < 4; ++i) pc.w[n * 4 + i] = y[i];
-                if constexpr (MX) pc.e[n] = ks[r / 32 + x % PC::KP / 2];
             }
         };
-        auto load_v = [&](int32_t row) {
+        auto load_v = [&](PC& pc, int32_t row) {
 #pragma unroll
             for (int n = 0; n < PC::VN; ++n) {
                 int kb, gg, s, ch;
@@ -196,29 +199,44 @@ __global__ void __launch_bounds__(64 * NW, D == 256 && NW == 4 ? 1 : 2) wide_ker
                     } else {
                         w[0] = *reinterpret_cast<const uint32_t*>(p);
                     }
-                    if constexpr (MX) pc.e[PC::E0 + n * 4 + j] = vs[r / 32 + ch * PL::CW / 32];
                 }
             }
         };
+        const bool loads_v = PC::SPLIT ? wave < 4 : (lane >> 4) & 1;
+        auto load_scales = [&](PC& pc, int32_t row) {
+            const int i = lane & 15, w4 = t8 >> 6;
+            const int y = (i / PC::VK * 256 + w4 * 64) / PC::VP + i % PC::VK / 4;
+            const int key = loads_v ? (y >> 3) * 32 + (y & 1) * 16 + ((y >> 1) & 3) * 4 + (i & 3)
+                                    : (i / PC::KK * 256 + w4 * 64) / PC::KP + i % PC::KK;
+            const uint8_t* p = (loads_v ? vs : ks) + row_of_key(row, key) / 32;
+            if constexpr (D == 64) pc.scale = *reinterpret_cast<const uint16_t*>(p);
+            else pc.scale = *reinterpret_cast<const uint32_t*>(p + (D > 128 ? lane >> 5 : 0) * 4);
+        };
+        // Byte `byte` of the scales of the wave's key i, of V or K.
+        auto scale_of = [&](const PC& pc, bool v, int i, int byte) {
+            const uint32_t w = __shfl(pc.scale, (byte >> 2) * 32 + (v && !PC::SPLIT ? 16 : 0) + i);
+            return e8m0((w >> ((byte & 3) * 8)) & 255u);
+        };
         // (a slot of -1 is loaded as row 0, which a pool with pages has)
-        auto load = [&](int32_t slots) {
+        auto load = [&](PC& pc, int32_t slots) {
             const int32_t row = slots < 0 ? 0 : slots;
+            if constexpr (MX) load_scales(pc, row);
             if constexpr (PC::SPLIT) {
-                if (wave < 4) load_v(row);
-                else load_k(row);
+                if (wave < 4) load_v(pc, row);
+                else load_k(pc, row);
             } else {
-                load_k(row);
-                load_v(row);
+                load_k(pc, row);
+                load_v(pc, row);
             }
         };
-        auto store_k = [&](int buf) {
+        auto store_k = [&](const PC& pc, int buf) {
 #pragma unroll
             for (int n = 0; n < PC::KN; ++n) {
                 const int x = n * 256 + t8;
                 const int key = x / PC::KP, piece = x % PC::KP;
                 const uint32_t* w = pc.w + n * 4;
                 if constexpr (MX) {
-                    const float e = e8m0(pc.e[n]);
+                    const float e = scale_of(pc, false, n * PC::KK + lane / PC::KP, lane % PC::KP / 2);
 #pragma unroll
                     for (int i = 0; i < 2; ++i)
                         *reinterpret_cast<u32x4*>(kbuf[buf] + PL::k(key, piece * 2 + i)) = u32x4{
@@ -230,7 +248,7 @@ __global__ void __launch_bounds__(64 * NW, D == 256 && NW == 4 ? 1 : 2) wide_ker
                 }
             }
         };
-        auto store_v = [&](int buf, int32_t step, uint64_t valid) {
+        auto store_v = [&](const PC& pc, int buf, int32_t step, uint64_t valid) {
             const bool plain = valid == ~0ull && (int64_t)(step + 1) * kKeys <= q.ctx;
 #pragma unroll
             for (int n = 0; n < PC::VN; ++n) {
@@ -239,16 +257,17 @@ __global__ void __launch_bounds__(64 * NW, D == 256 && NW == 4 ? 1 : 2) wide_ker
                 constexpr int CP = PL::CW / 2;
                 uint32_t w[4][CP];  // [key][channel pair]
 #pragma unroll
-                for (int j = 0; j < 4; ++j)
+                for (int j = 0; j < 4; ++j) {
+                    float scale = 1.0f;
+                    if constexpr (MX)
+                        scale = scale_of(pc, true, n * PC::VK + lane / PC::VP * 4 + j, ch * PL::CW / 32);
 #pragma unroll
                     for (int i = 0; i < CP; ++i) {
                         const uint32_t* from = pc.w + PC::V0 + (n * 4 + j) * PC::VW;
-                        if constexpr (MX)
-                            w[j][i] =
-                                X::widen2(from[i / 2], e8m0(pc.e[PC::E0 + n * 4 + j]), i & 1);
-                        else
-                            w[j][i] = from[i];
+                        if constexpr (MX) w[j][i] = X::widen2(from[i / 2], scale, i & 1);
+                        else w[j][i] = from[i];
                     }
+                }
                 if (!plain) {
                     // Keys that do not exist count as zeros. Among the new tokens a row of V may
                     // be one that only some query rows look at, and an infinity or a NaN times
@@ -280,13 +299,13 @@ __global__ void __launch_bounds__(64 * NW, D == 256 && NW == 4 ? 1 : 2) wide_ker
                 }
             }
         };
-        auto store = [&](int buf, int32_t step, uint64_t valid) {
+        auto store = [&](const PC& pc, int buf, int32_t step, uint64_t valid) {
             if constexpr (PC::SPLIT) {
-                if (wave < 4) store_v(buf, step, valid);
-                else store_k(buf);
+                if (wave < 4) store_v(pc, buf, step, valid);
+                else store_k(pc, buf);
             } else {
-                store_k(buf);
-                store_v(buf, step, valid);
+                store_k(pc, buf);
+                store_v(pc, buf, step, valid);
             }
         };
 
@@ -394,27 +413,35 @@ __global__ void __launch_bounds__(64 * NW, D == 256 && NW == 4 ? 1 : 2) wide_ker
         if (tid == 0) left_out_any = 0;
         if (q.keys > 0 && a.pg.num_pages > 0) {
             // (steps past the last are loaded as row 0 and count as no keys)
-            int32_t slots = row_slot(fetch(step0), step0);
-            int32_t page = fetch(step0 + 1);
-            uint64_t now = __ballot(slots >= 0);
-            load(slots);
+            int32_t page = fetch(step0);
+            auto load_next = [&](int32_t step) {  // the step after those under way
+                const int32_t slots = row_slot(page, step);
+                page = fetch(step + 1);
+                load(pc, slots);
+                return (uint64_t)__ballot(slots >= 0);
+            };
+            uint64_t now = load_next(step0), next = 0;
             __syncthreads();  // left_out_any is cleared
-            store(0, step0, now);
-            slots = row_slot(page, step0 + 1);
-            page = fetch(step0 + 2);
-            uint64_t next = __ballot(slots >= 0);
-            load(slots);
-            __syncthreads();
+            if constexpr (BUFS == 2) {
+                store(pc, 0, step0, now);
+                next = load_next(step0 + 1);
+                __syncthreads();
+            }
             for (int32_t step = step0; step < step1; ++step) {
-                const int buf = (step - step0) & 1;
-                store(buf ^ 1, step + 1, next);
-                slots = row_slot(page, step + 2);
-                page = fetch(step + 3);
-                const uint64_t after = __ballot(slots >= 0);
-                load(slots);
-                if (now && mine > 0) compute(buf, step, now);
-                now = next;
-                next = after;
+                if constexpr (BUFS == 2) {
+                    const int buf = (step - step0) & 1;
+                    store(pc, buf ^ 1, step + 1, next);
+                    const uint64_t after = load_next(step + 2);
+                    if (now && mine > 0) compute(buf, step, now);
+                    now = next;
+                    next = after;
+                } else {
+                    store(pc, 0, step, now);
+                    next = load_next(step + 1);
+                    __syncthreads();
+                    if (now && mine > 0) compute(0, step, now);
+                    now = next;
+                }
                 __syncthreads();
             }
         } else {
