@@ -104,7 +104,7 @@ struct RunScratch {
 
 // By the whole workgroup: the cost of all sequences; in `scratch` the sequence that this worker's run
 // begins in and that sequence's place in the line. The first worker leaves the prefix sums for the
-// joining launch in `prefix`.
+// joining launch, if there is one, in `prefix`.
 template <class S, int WORKERS, int THREADS>
 __device__ inline int64_t find_run(const AttnArgs& a, int64_t* prefix, RunScratch& scratch) {
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
@@ -138,10 +138,10 @@ __device__ inline int64_t find_run(const AttnArgs& a, int64_t* prefix, RunScratc
             scratch.s = s;
             scratch.first = x;
         }
-        if (me == 0) prefix[s] = x;
+        if (me == 0 && prefix != nullptr) prefix[s] = x;
         x += n;
     }
-    if (me == 0 && tid == THREADS - 1) prefix[a.b.num_seqs] = total;
+    if (me == 0 && tid == THREADS - 1 && prefix != nullptr) prefix[a.b.num_seqs] = total;
     __syncthreads();
     return total;
 }
