@@ -277,11 +277,7 @@ __global__ void __launch_bounds__(THREADS) pick_kernel(SelectArgs a) {
     if (k > 0) {
         uint32_t threshold;
         int ties;
-        kth_of_registers<THREADS, KPT>(key, P, k, scratch, threshold, ties);
-        auto below = [](uint64_t mask) {  // bits of lower lanes
-            return (int)__builtin_amdgcn_mbcnt_hi((uint32_t)(mask >> 32),
-                                                  __builtin_amdgcn_mbcnt_lo((uint32_t)mask, 0));
-        };
+        kth_of_registers<THREADS, KPT>(key, usable, k, scratch, threshold, ties);
         auto scan = [&](int list) {  // counts of (i, wave) to places
             __syncthreads();
             const int n = tid < KPT * WAVES ? first[list][tid] : 0;
@@ -291,11 +287,7 @@ __global__ void __launch_bounds__(THREADS) pick_kernel(SelectArgs a) {
             return total;
         };
         if (ties > 0) {  // the lowest of the equal pages
-#pragma unroll
-            for (int i = 0; i < KPT; ++i) {
-                const uint64_t m = __ballot(key[i] == threshold);
-                if ((tid & 63) == 0) first[0][i * WAVES + wave] = __builtin_popcountll(m);
-            }
+            put_counts<WAVES, KPT>(first[0], [&](int i) { return key[i] == threshold; });
             scan(0);
         }
 #pragma unroll
@@ -303,17 +295,16 @@ __global__ void __launch_bounds__(THREADS) pick_kernel(SelectArgs a) {
             bool keep = key[i] > threshold;
             if (ties > 0) {
                 const bool tie = key[i] == threshold;
-                keep |= tie && first[0][i * WAVES + wave] + below(__ballot(tie)) < ties;
+                keep |= tie && first[0][i * WAVES + wave] + lanes_below(__ballot(tie)) < ties;
             }
-            const uint64_t m = __ballot(keep);
-            if ((tid & 63) == 0) first[1][i * WAVES + wave] = __builtin_popcountll(m);
             key[i] = keep;
         }
+        put_counts<WAVES, KPT>(first[1], [&](int i) { return key[i] != 0; });
         done = scan(1);
 #pragma unroll
         for (int i = 0; i < KPT; ++i) {
             const uint64_t m = __ballot(key[i] != 0);
-            if (key[i]) out[first[1][i * WAVES + wave] + below(m)] = i * THREADS + tid;
+            if (key[i]) out[first[1][i * WAVES + wave] + lanes_below(m)] = i * THREADS + tid;
         }
     }
     for (int j = done + tid; j < a.topk; j += THREADS) out[j] = -1;

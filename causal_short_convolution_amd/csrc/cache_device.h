@@ -163,12 +163,28 @@ __device__ inline void kth_largest(Key key, int n, int k, uint32_t* hist, uint32
     ties = rest;
 }
 
+// Bits of a wave's mask for lanes below this one.
+__device__ inline int lanes_below(uint64_t mask) {
+    return (int)__builtin_amdgcn_mbcnt_hi((uint32_t)(mask >> 32),
+                                          __builtin_amdgcn_mbcnt_lo((uint32_t)mask, 0));
+}
+
+// Leaves the wave's counts of N flags per lane in `counts`[i * WAVES + wave]. (All lanes store the
+// one value: no branch, and no lane mask held for each.)
+template <int WAVES, int N, class F>
+__device__ inline void put_counts(int* counts, F flag) {
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+        counts[i * WAVES + (threadIdx.x >> 6)] = __builtin_popcountll(__ballot(flag(i)));
+}
+
 // LDS of kth_of_registers.
 struct KthScratch {
     static constexpr int kList = 1024;
     uint32_t list[kList];
     int counts[2][16];
-    uint32_t used, differ;
+    uint32_t ends[2][16];
+    uint32_t used;
 };
 
 // Keys of the workgroup at or above `cand`, in every thread: a compare per key and a population
@@ -190,86 +206,105 @@ __device__ inline int count_at_least(const uint32_t (&key)[KPT], uint32_t cand, 
     return uniform(n);
 }
 
-// The k-th largest of n keys that a workgroup of THREADS threads holds in registers, key
-// i * THREADS + threadIdx.x in register i (0 past the n-th), 1 <= k <= n: bit by bit from the top, each bit kept if at least k keys reach the
-// value with it. Once few enough keys can still be it, those go to LDS and the remaining bits are
-// found among them, from the highest bit they differ in. Returns `threshold` and `ties`: the k
-// largest are the keys above the threshold and `ties` of those equal to it.
+// The k-th largest key lies in [lo, hi]: `reach` >= k keys are at or above lo, `above` < k are past
+// hi. Halves the range while more than `stop` keys are left in it; true once the k largest are
+// exactly the keys from lo on.
+struct KeyRange {
+    uint32_t lo, hi;
+    int reach, above;
+};
+template <int THREADS, int KPT>
+__device__ inline bool halve_range(const uint32_t (&key)[KPT], int others, int k, int stop,
+                                   KeyRange& r, int& turn, KthScratch& sc) {
+    while (r.lo < r.hi && r.reach - r.above > stop) {
+        const uint32_t mid = r.lo + ((r.hi - r.lo) >> 1) + 1;
+        const int c = others + count_at_least<THREADS, KPT>(key, mid, ++turn, sc);
+        if (c >= k) {
+            r.lo = mid;
+            r.reach = c;
+        } else {
+            r.hi = mid - 1;
+            r.above = c;
+        }
+        if (c == k) return true;
+    }
+    return false;
+}
+
+// The k-th largest of the n keys that a workgroup of THREADS threads holds in registers, where 0 is
+// no key, 1 <= k <= n: the range between the least
+// and the largest key (but for keys of all ones, which are counted first) is halved by value until
+// few enough are left; those go to LDS and the search ends among them. Returns `threshold` and
+// `ties`: the k largest are the keys above the threshold and `ties` of those equal to it.
 template <int THREADS, int KPT>
 __device__ inline void kth_of_registers(const uint32_t (&key)[KPT], int n, int k, KthScratch& sc,
                                         uint32_t& threshold, int& ties) {
+    constexpr int WAVES = THREADS / 64;
     constexpr int LPT = KthScratch::kList / THREADS;
-    uint32_t t = 0;
-    int above = 0;    // keys past those that can still be the k-th largest
-    int reach = n;    // keys at or above t
-    int bit = 31;
-    __syncthreads();
-    if (threadIdx.x == 0) sc.used = sc.differ = 0;
-    for (; bit >= 0 && reach - above > KthScratch::kList; --bit) {
-        const uint32_t cand = t | (1u << bit);
-        const int c = count_at_least<THREADS, KPT>(key, cand, bit, sc);
-        if (c >= k) {
-            t = cand;
-            reach = c;
-        } else {
-            above = c;
-        }
-        if (c == k) {  // exactly the keys from here on
-            threshold = cand - 1;
-            ties = 0;
-            return;
-        }
-    }
-    if (bit < 0) {
-        threshold = t;
-        ties = k - above;
-        return;
-    }
-    __syncthreads();  // `used` is cleared, and no wave still reads the counts
-    const uint32_t span = bit == 31 ? 0xffffffffu : (2u << bit) - 1u;  // keys t .. t + span are left
+    KeyRange r{0xffffffffu, 0u, n, 0};
 #pragma unroll
     for (int i = 0; i < KPT; ++i) {
-        // key >= t and key <= t + span, unsigned
-        const bool left = i * THREADS + (int)threadIdx.x < n && key[i] - t <= span;
-        const uint64_t m = __ballot(left);
-        if (m == 0) continue;
-        uint32_t at = 0;
-        if ((threadIdx.x & 63) == 0) at = atomicAdd(&sc.used, (uint32_t)__builtin_popcountll(m));
-        at = (uint32_t)uniform((int32_t)at) +
-             __builtin_amdgcn_mbcnt_hi((uint32_t)(m >> 32),
-                                       __builtin_amdgcn_mbcnt_lo((uint32_t)m, 0));
-        if (left && at < KthScratch::kList) sc.list[at] = key[i];
+        const bool top = key[i] == 0xffffffffu;
+        r.above += __builtin_popcountll(__ballot(top));
+        r.lo = min(r.lo, key[i] - 1);  // (0 is the largest here)
+        r.hi = max(r.hi, top ? 0u : key[i]);
     }
+    r.lo = ~head_max<64>(~r.lo) + 1;
+    r.hi = head_max<64>(r.hi);
+    if (r.lo == 0) r.lo = 0xffffffffu;  // a wave without keys
+    __syncthreads();  // the scratch is free
+    if ((threadIdx.x & 63) == 0) {
+        sc.counts[0][threadIdx.x >> 6] = r.above;
+        sc.ends[0][threadIdx.x >> 6] = r.lo;
+        sc.ends[1][threadIdx.x >> 6] = r.hi;
+    }
+    if (threadIdx.x == 0) sc.used = 0;
     __syncthreads();
-    const int used = min((int)sc.used, KthScratch::kList);
-    const uint32_t probe = sc.list[0];
-    uint32_t mine[LPT], differ = 0;
+    r = KeyRange{0xffffffffu, 0u, n, 0};
 #pragma unroll
-    for (int i = 0; i < LPT; ++i) {
-        const int j = i * THREADS + threadIdx.x;
-        mine[i] = j < used ? sc.list[j] : 0u;
-        if (j < used) differ |= mine[i] ^ probe;
+    for (int w = 0; w < WAVES; ++w) {
+        r.above += sc.counts[0][w];
+        r.lo = min(r.lo, sc.ends[0][w]);
+        r.hi = max(r.hi, sc.ends[1][w]);
     }
-    if (__ballot(differ != 0)) atomicOr(&sc.differ, differ);
-    __syncthreads();
-    differ = sc.differ;
-    // the bits that all share are the k-th largest's too
-    const int high = differ ? 31 - __builtin_clz(differ) : -1;
-    t = high == 31 ? 0u : high < 0 ? probe : probe & ~((2u << high) - 1u);
-    for (bit = high; bit >= 0; --bit) {
-        const uint32_t cand = t | (1u << bit);
-        const int c = above + count_at_least<THREADS, LPT>(mine, cand, bit, sc);
-        if (c >= k) t = cand;
-        if (c == k) {
-            threshold = cand - 1;
-            ties = 0;
-            return;
+    r = KeyRange{(uint32_t)uniform((int32_t)r.lo), (uint32_t)uniform((int32_t)r.hi), n,
+                 uniform(r.above)};
+    if (r.above >= k) {
+        threshold = 0xffffffffu;
+        ties = k;
+        return;
+    }
+    int turn = 0;  // (the counts above were the even half)
+    bool exact = halve_range<THREADS, KPT>(key, 0, k, KthScratch::kList, r, turn, sc);
+    if (!exact && r.lo < r.hi) {
+        const uint32_t lo = r.lo, span = r.hi - r.lo;
+        const int others = r.above;  // keys past the range
+        auto left = [&](int i) { return key[i] - lo <= span; };  // unsigned: lo <= key <= hi
+        int n_left = 0;
+#pragma unroll
+        for (int i = 0; i < KPT; ++i) n_left += __builtin_popcountll(__ballot(left(i)));
+        int at = 0;  // the wave's place in the list
+        if ((threadIdx.x & 63) == 0) at = (int)atomicAdd(&sc.used, (uint32_t)n_left);
+        at = uniform(at);
+#pragma unroll
+        for (int i = 0; i < KPT; ++i) {
+            const uint64_t m = __ballot(left(i));
+            const int place = at + lanes_below(m);
+            if (left(i) && place < KthScratch::kList) sc.list[place] = key[i];
+            at += __builtin_popcountll(m);
         }
+        __syncthreads();
+        const int used = min((int)sc.used, KthScratch::kList);
+        uint32_t mine[LPT];
+#pragma unroll
+        for (int i = 0; i < LPT; ++i) {
+            const int j = i * THREADS + threadIdx.x;
+            mine[i] = j < used ? sc.list[j] : 0u;  // (0 is below every middle)
+        }
+        exact = halve_range<THREADS, LPT>(mine, others, k, 0, r, turn, sc);
     }
-    int more = 0;
-    if (t != 0xffffffffu) more = count_at_least<THREADS, LPT>(mine, t + 1, bit, sc);
-    threshold = t;
-    ties = k - above - more;
+    threshold = exact ? r.lo - 1 : r.lo;
+    ties = exact ? 0 : k - r.above;
 }
 
 // Exclusive prefix sum over the workgroup of one small count per thread, and the total. `sums` is

@@ -39,10 +39,11 @@ struct Head {
         late = (int64_t)a.seen[s] - a.recent;
         sinks = a.sinks;
     }
-    // Protected entries above all numbers, NaN below them.
+    // Protected entries above all numbers, NaN below them; 0 is no entry.
     __device__ uint32_t key(float f, int32_t pos) const {
-        if (pos < sinks || pos >= late) return 0xffffffffu;
-        return f != f ? 0u : order_key(f);
+        const uint32_t k = f != f ? 1u : order_key(f);
+        const bool safe = (pos < sinks) | (pos >= late);  // (no branch for each entry)
+        return safe ? 0xffffffffu : k;
     }
     // Scores and positions of the kept entries: those that stay (unless the output is the input),
     // then those that move, whose sources lie at or past the budget.
@@ -109,10 +110,6 @@ __global__ void __launch_bounds__(THREADS) evict_plan_kernel(EvictArgs a) {
         uint32_t threshold;
         int ties, total;
         kth_of_registers<THREADS, KPT>(key, n, kept, scratch, threshold, ties);
-        auto below = [](uint64_t mask) {  // bits of lower lanes
-            return (int)__builtin_amdgcn_mbcnt_hi((uint32_t)(mask >> 32),
-                                                  __builtin_amdgcn_mbcnt_lo((uint32_t)mask, 0));
-        };
         auto scan = [&](int list) {
             __syncthreads();
             static_assert(KPT * WAVES <= THREADS, "one count per thread");
@@ -123,43 +120,33 @@ __global__ void __launch_bounds__(THREADS) evict_plan_kernel(EvictArgs a) {
             return total;
         };
         if (ties > 0) {  // the lowest of the equal entries
-#pragma unroll
-            for (int i = 0; i < KPT; ++i) {
-                const uint64_t m = __ballot(key[i] == threshold && i * THREADS + tid < n);
-                if ((tid & 63) == 0) first[0][i * WAVES + wave] = __builtin_popcountll(m);
-            }
+            put_counts<WAVES, KPT>(first[0], [&](int i) {
+                return key[i] == threshold;
+            });
             scan(0);
         }
 #pragma unroll
         for (int i = 0; i < KPT; ++i) {  // from here on key[i] is 1 for an entry to keep
             bool keep = key[i] > threshold;
             if (ties > 0) {
-                const bool tie = key[i] == threshold && i * THREADS + tid < n;
-                keep |= tie && first[0][i * WAVES + wave] + below(__ballot(tie)) < ties;
+                const bool tie = key[i] == threshold;
+                keep |= tie && first[0][i * WAVES + wave] + lanes_below(__ballot(tie)) < ties;
             }
             key[i] = keep;
         }
         __syncthreads();
-#pragma unroll
-        for (int i = 0; i < KPT; ++i) {
-            const int j = i * THREADS + tid;
-            const uint64_t hole = __ballot(!key[i] && j < kept);
-            const uint64_t move = __ballot(key[i] && j >= kept);
-            if ((tid & 63) == 0) {
-                first[0][i * WAVES + wave] = __builtin_popcountll(hole);
-                first[1][i * WAVES + wave] = __builtin_popcountll(move);
-            }
-        }
+        auto is_hole = [&](int i) { return !key[i] & (i * THREADS + tid < kept); };
+        auto is_move = [&](int i) { return (key[i] != 0) & (i * THREADS + tid >= kept); };
+        put_counts<WAVES, KPT>(first[0], is_hole);
+        put_counts<WAVES, KPT>(first[1], is_move);
         holes = scan(0);
         scan(1);
 #pragma unroll
         for (int i = 0; i < KPT; ++i) {
             const int j = i * THREADS + tid;
-            const bool hole = !key[i] && j < kept;
-            const bool move = key[i] && j >= kept;
-            const uint64_t mh = __ballot(hole), mm = __ballot(move);
-            if (hole) head.dst[first[0][i * WAVES + wave] + below(mh)] = j;
-            if (move) head.src[first[1][i * WAVES + wave] + below(mm)] = j;
+            const uint64_t mh = __ballot(is_hole(i)), mm = __ballot(is_move(i));
+            if (is_hole(i)) head.dst[first[0][i * WAVES + wave] + lanes_below(mh)] = j;
+            if (is_move(i)) head.src[first[1][i * WAVES + wave] + lanes_below(mm)] = j;
         }
         __syncthreads();
     }

@@ -24,7 +24,7 @@ __device__ inline float sum16(float v) {
 
 // The steps of 4 wave tiles of all (sequence, cache head) lie in one line that the workgroups share
 // out evenly, as in the attention, so ragged lengths fill the chip to the end: 4 workgroups on each
-// CU where LDS holds the queries of 4, else 2.
+// CU (a fourth took spilled registers, 67 us for 58), 2 where their queries fill LDS.
 // (A sequence without new tokens has its keys' scores carried over, so its keys count too.)
 template <int KS>
 struct KeySteps : Steps<KS, 1 << 30, 0> {
