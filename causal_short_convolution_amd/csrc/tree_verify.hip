@@ -25,13 +25,16 @@ __global__ void __launch_bounds__(kBlock) verify_tree_kernel(StepArgs a, VerifyA
     const int32_t i = (int32_t)(t - start);
 
     if (ta.mask != nullptr && blockIdx.y == 0 && threadIdx.x == 0) {
-        for (int w = 0; w < ta.words; ++w) {
+        // one walk to the root: a token's ancestors have lower indices
+        auto parent = [&](int32_t j) {
+            const int32_t p = ta.parents[start + j];
+            return p < j ? p : -1;
+        };
+        int32_t j = i;
+        for (int w = ta.words - 1; w >= 0; --w) {
             uint64_t bits = 0;
-            for (int32_t j = i; j >= 0;) {
-                if ((j >> 6) == w) bits |= 1ull << (j & 63);
-                const int32_t p = ta.parents[start + j];
-                j = p < j ? p : -1;
-            }
+            while (j >= 0 && (j >> 6) > w) j = parent(j);  // past the mask
+            for (; j >= 0 && (j >> 6) == w; j = parent(j)) bits |= 1ull << (j & 63);
             ta.mask[t * ta.words + w] = (int64_t)bits;
         }
     }
