@@ -128,12 +128,12 @@ __global__ void __launch_bounds__(kBlock) summary_kernel(SummaryArgs a) {
 typedef int32_t i32x4 __attribute__((ext_vector_type(4)));
 constexpr int kTokens = 16;  // tokens of one sequence per workgroup
 
+// 16 bytes of a query as fp32; a NaN counts as 0.
 template <class E>
-__device__ inline float query_element(const char* base, int j) {  // a NaN counts as 0
-    const float f = E::BYTES == 4
-                        ? reinterpret_cast<const float*>(base)[j]
-                        : __uint_as_float((uint32_t) reinterpret_cast<const uint16_t*>(base)[j] << 16);
-    return f != f ? 0.0f : f;
+__device__ inline void load_query(const char* p, float (&f)[E::VEC]) {
+    E::widen(*reinterpret_cast<const uint4*>(p), f);
+#pragma unroll
+    for (int v = 0; v < E::VEC; ++v) f[v] = f[v] != f[v] ? 0.0f : f[v];
 }
 
 // Workgroup: tile blockIdx.x of kTokens tokens (tiles do not cross sequences), head blockIdx.y,
@@ -155,27 +155,41 @@ __global__ void __launch_bounds__(kBlock) score_kernel(SelectArgs a) {
     const int n = (int)min((int64_t)kTokens, q.len - i0);
     const int64_t t0 = q.start + i0;
 
-    // ---- the tokens' codes: 4 tokens per wave, one after the other
-    for (int k = wave; k < kTokens; k += 4) {
+    // ---- the tokens' codes: token 4 wave + g by the 16 lanes of group g (columns past the last
+    // token are multiplied too, and not looked at)
+    if (const int k = 4 * wave + g; k < n) {
+        constexpr int VEC = E::VEC;
         const char* base = static_cast<const char*>(a.q) +
-                           ((t0 + min(k, n - 1)) * a.q_stride + (int64_t)h * a.group * D) * E::BYTES;
+                           ((t0 + k) * a.q_stride + (int64_t)h * a.group * D) * E::BYTES;
+        float f[VEC];
         uint32_t top = 0;
-        for (int j = lane; j < a.group * D; j += 64)
-            top = max(top, __float_as_uint(__builtin_fabsf(query_element<E>(base, j))));
-        const int e = code_exponent(head_max<64>(top));
-        for (int d = lane; d < D; d += 64) {
-            int below = 0, above = 0;
+        for (int j = c * VEC; j < a.group * D; j += 16 * VEC) {
+            load_query<E>(base + j * E::BYTES, f);
+#pragma unroll
+            for (int v = 0; v < VEC; ++v) top = max(top, __float_as_uint(__builtin_fabsf(f[v])));
+        }
+        const int e = code_exponent(head_max<16>(top));
+        for (int d = c * VEC; d < D; d += 16 * VEC) {
+            int below[VEC], above[VEC];
+#pragma unroll
+            for (int v = 0; v < VEC; ++v) below[v] = above[v] = 0;
             for (int x = 0; x < a.group; ++x) {
-                const int v = (int)code_of(query_element<E>(base, x * D + d), e);
-                below += min(v, 0);
-                above += max(v, 0);
+                load_query<E>(base + (x * D + d) * E::BYTES, f);
+#pragma unroll
+                for (int v = 0; v < VEC; ++v) {
+                    const int y = (int)code_of(f[v], e);
+                    below[v] += min(y, 0);
+                    above[v] += max(y, 0);
+                }
             }
 #pragma unroll
-            for (int p = 0; p < PLANES; ++p) {
-                const bool last = p == PLANES - 1;
-                code[p][k][d] = (int8_t)(last ? below >> (6 * p) : (below >> (6 * p)) & 63);
-                code[p][k][D + d] = (int8_t)(last ? above >> (6 * p) : (above >> (6 * p)) & 63);
-            }
+            for (int p = 0; p < PLANES; ++p)
+#pragma unroll
+                for (int v = 0; v < VEC; ++v) {
+                    const bool last = p == PLANES - 1;
+                    code[p][k][d + v] = (int8_t)(last ? below[v] >> (6 * p) : (below[v] >> (6 * p)) & 63);
+                    code[p][k][D + d + v] = (int8_t)(last ? above[v] >> (6 * p) : (above[v] >> (6 * p)) & 63);
+                }
         }
     }
     __syncthreads();
@@ -193,9 +207,12 @@ __global__ void __launch_bounds__(kBlock) score_kernel(SelectArgs a) {
     const int32_t own = (int32_t)min((int64_t)a.pg.max_blocks,
                                      (((int64_t)q.ctx + i0 + c) >> a.pg.shift) + 1);
     uint32_t* keys = a.keys + ((t0 + c) * a.heads + h) * a.key_stride;
-    for (int32_t p0 = (blockIdx.z * 4 + wave) * 16; p0 < pages; p0 += gridDim.z * 64) {
-        const int32_t pb = p0 + c;
-        const int32_t page = pb < pages ? table[pb] : -1;
+    auto page_at = [&](int32_t pb) { return pb < pages ? table[pb] : -1; };
+    const int32_t first = (blockIdx.z * 4 + wave) * 16, stride = gridDim.z * 64;
+    int32_t next = page_at(first + c);
+    for (int32_t p0 = first; p0 < pages; p0 += stride) {
+        const int32_t page = next;
+        next = page_at(p0 + stride + c);
         const bool ok = page >= 0 && page < a.pg.num_pages;
         const int64_t at = (int64_t)(ok ? page : 0) * a.heads + h;
         i32x4 row[NF];
