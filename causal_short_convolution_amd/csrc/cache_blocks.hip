@@ -33,6 +33,7 @@ struct KeyRow {
     }
 };
 
+// Bound by the bytes of K: 65000 MXFP8 keys of 8 heads of 128 in 20 us (3.3 TB/s).
 // Workgroup: one 64-lane column slice of a page (blockIdx.x strides over the pages of sequence
 // blockIdx.y); its 4 waves take every fourth row and meet in LDS.
 template <class E, int D, bool MX>
@@ -136,6 +137,8 @@ __device__ inline void load_query(const char* p, float (&f)[E::VEC]) {
     for (int v = 0; v < E::VEC; ++v) f[v] = f[v] != f[v] ? 0.0f : f[v];
 }
 
+// 512 tokens against 1016 pages of 8 heads of 128 take 20 us, and picking 32 of them 18 us; one kernel
+// with a thread per page, plain dot products and a histogram in LDS took 290.
 // Workgroup: tile blockIdx.x of kTokens tokens (tiles do not cross sequences), head blockIdx.y,
 // every gridDim.z-th group of 4 x 16 pages.
 template <class E, int D, int PLANES>
@@ -254,7 +257,8 @@ __global__ void __launch_bounds__(kBlock) score_kernel(SelectArgs a) {
 }
 
 // ------------------------------------------------------------------------------------------------
-// The pages with the largest keys, one workgroup per (token, cache head).
+// The pages with the largest keys, one workgroup per (token, cache head). One wave where its registers
+// hold the row: the meetings of several waves cost more than their help.
 // ------------------------------------------------------------------------------------------------
 __device__ inline int token_pages(const SelectArgs& a, int64_t t) {
     const int s = seq_of_token(a.b, t);

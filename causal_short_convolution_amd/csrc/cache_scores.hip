@@ -4,6 +4,8 @@
 // of the cache head, 16 at a time from LDS; logits as in the attention (S^T = K Q^T, the lane holds
 // query row lane % 16), weights summed per lane over the row tiles and over the 16 rows at the end.
 // K is read once, nothing is shared between waves but the queries, and there is nothing to join.
+// Measured: 64 sequences of 1-8192 MXFP8 keys, 8 heads of 128 with 4 rows each, 80 us (3.9 TB/s of
+// keys); 16 sequences of 2000-8192 bf16 keys with 128 rows, 54 us (3.3 TB/s).
 #include "attention_line.h"
 
 namespace sc {

@@ -5,9 +5,16 @@
 // cache_attention.hip, which each stream their own keys, would each hold all rows. Here a step of
 // 64 keys is brought in once per workgroup, into LDS in the form in which the products take it:
 // K by rows, V transposed (rows of channels, keys in the order in which the lane of a query row
-// holds their weights), both in bf16 whatever the cache holds. Two such buffers alternate: while
-// step t is computed from one, step t + 1, loaded to registers a step earlier, is written to the
-// other, and the loads of step t + 2 (with 4 waves, of t + 3 too) are under way. One barrier per step.
+// holds their weights), both in bf16 whatever the cache holds. With 8 waves two such buffers
+// alternate: while step t is computed from one, step t + 1, loaded to registers a step earlier, is
+// written to the other, and the loads of step t + 2 are under way; one barrier per step. With 4 waves
+// (D <= 128) there is one buffer, written between two barriers while the next step's loads are under way:
+// LDS and registers then hold three workgroups on a CU, whose phases overlap better than those of
+// two with two buffers (64 sequences x 64 rows over 512-8192 MXFP8 keys of 8 heads: 189 against 207 us;
+// loads two steps ahead changed nothing).
+//
+// Measured: 2 x 256 rows over 131072 keys of 8 heads of 128, bf16: 500-545 us, 0.5 PFLOP/s, 65 % of
+// the issue slots taken, 44 % of the matrix cores' time.
 //
 // Rows in LDS are not padded; their 16-byte pieces are permuted by exclusive or with bits of the row,
 // so that the lanes that an access serves at a time fall on different banks: 16 rows of one piece
