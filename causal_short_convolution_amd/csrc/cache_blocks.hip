@@ -210,10 +210,10 @@ __global__ void __launch_bounds__(kBlock) score_kernel(SelectArgs a) {
     const int32_t own = (int32_t)min((int64_t)a.pg.max_blocks,
                                      (((int64_t)q.ctx + i0 + c) >> a.pg.shift) + 1);
     uint32_t* keys = a.keys + ((t0 + c) * a.heads + h) * a.key_stride;
-    auto page_at = [&](int32_t pb) { return pb < pages ? table[pb] : -1; };
-    const int32_t first = (blockIdx.z * 4 + wave) * 16, stride = gridDim.z * 64;
+    auto page_at = [&](uint32_t pb) { return pb < (uint32_t)pages ? table[pb] : -1; };
+    const uint32_t first = (blockIdx.z * 4 + wave) * 16, stride = gridDim.z * 64;
     int32_t next = page_at(first + c);
-    for (int32_t p0 = first; p0 < pages; p0 += stride) {
+    for (uint32_t p0 = first; p0 < (uint32_t)pages; p0 += stride) {
         const int32_t page = next;
         next = page_at(p0 + stride + c);
         const bool ok = page >= 0 && page < a.pg.num_pages;
@@ -241,7 +241,7 @@ __global__ void __launch_bounds__(kBlock) score_kernel(SelectArgs a) {
         uint32_t key[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const int32_t b = p0 + g * 4 + i;
+            const int32_t b = (int32_t)p0 + g * 4 + i;
             const int eb = __shfl(e, g * 4 + i);
             const bool usable = __shfl((int)ok, g * 4 + i);
             const bool forced = b < a.sinks || b >= (int64_t)own - a.recents;
@@ -249,7 +249,7 @@ __global__ void __launch_bounds__(kBlock) score_kernel(SelectArgs a) {
             if (!usable || b >= own) key[i] = 0;  // below every score: never chosen
         }
         if (c < n) {  // (rows of keys are padded to whole groups of 4)
-            if (p0 + g * 4 < pages)
+            if (p0 + g * 4 < (uint32_t)pages)
                 *reinterpret_cast<uint4*>(keys + p0 + g * 4) =
                     make_uint4(key[0], key[1], key[2], key[3]);
         }
