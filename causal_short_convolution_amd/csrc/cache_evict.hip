@@ -136,19 +136,33 @@ __global__ void __launch_bounds__(THREADS) evict_plan_kernel(EvictArgs a) {
             }
             key[i] = keep;
         }
-        __syncthreads();
-        auto is_hole = [&](int i) { return !key[i] & (i * THREADS + tid < kept); };
-        auto is_move = [&](int i) { return (key[i] != 0) & (i * THREADS + tid >= kept); };
-        put_counts<WAVES, KPT>(first[0], is_hole);
-        put_counts<WAVES, KPT>(first[1], is_move);
-        holes = scan(0);
-        scan(1);
+        // Holes and movers of register i in the wave, as masks; scalar work but for one comparison.
+        auto split = [&](int i, uint64_t& hole, uint64_t& move) {
+            const uint64_t m = __ballot(key[i] != 0);
+            const int n_low = kept - (i * THREADS + wave * 64);  // lanes below the budget
+            const uint64_t low = n_low >= 64 ? ~0ull : n_low <= 0 ? 0ull : (1ull << n_low) - 1;
+            hole = ~m & low;
+            move = m & ~low;
+        };
+        // Both counts in one word: there are as many of each, at most half of 65536 entries.
+        static_assert(THREADS * KPT <= 65536, "16 bits each");
 #pragma unroll
         for (int i = 0; i < KPT; ++i) {
+            uint64_t hole, move;
+            split(i, hole, move);
+            first[1][i * WAVES + wave] =
+                __builtin_popcountll(hole) | __builtin_popcountll(move) << 16;
+        }
+        holes = scan(1) & 0xffff;
+#pragma unroll
+        for (int i = 0; i < KPT; ++i) {
+            uint64_t hole, move;
+            split(i, hole, move);
+            if ((hole | move) == 0) continue;
+            const uint32_t at = (uint32_t)first[1][i * WAVES + wave];
             const int j = i * THREADS + tid;
-            const uint64_t mh = __ballot(is_hole(i)), mm = __ballot(is_move(i));
-            if (is_hole(i)) head.dst[first[0][i * WAVES + wave] + lanes_below(mh)] = j;
-            if (is_move(i)) head.src[first[1][i * WAVES + wave] + lanes_below(mm)] = j;
+            if (hole >> (tid & 63) & 1) head.dst[(at & 0xffff) + lanes_below(hole)] = j;
+            if (move >> (tid & 63) & 1) head.src[(at >> 16) + lanes_below(move)] = j;
         }
         __syncthreads();
     }
